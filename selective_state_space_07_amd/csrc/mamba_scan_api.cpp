@@ -14,12 +14,18 @@
 #include <cstring>
 #include <string>
 
+#include "api_checks.h"
 #include "scan_internal.h"
 
 namespace {
 
 thread_local std::string g_last_error;
 std::atomic<uint64_t> g_calls{0};
+
+}  // namespace
+
+namespace mscan {
+namespace api {
 
 int fail(int status, const char* fmt, ...) {
   char buf[512];
@@ -36,12 +42,11 @@ int ok() {
   return MAMBA_OK;
 }
 
-size_t io_size(int32_t io_dtype) { return io_dtype == MAMBA_BF16 ? 2 : 4; }
+std::string& last_error() { return g_last_error; }
 
-struct Range {
-  const char* name;
-  uintptr_t lo, hi;  // [lo, hi)
-};
+void count_call() { g_calls.fetch_add(1); }
+
+size_t io_size(int32_t io_dtype) { return io_dtype == MAMBA_BF16 ? 2 : 4; }
 
 Range range(const char* name, const void* p, size_t bytes) {
   const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
@@ -54,9 +59,6 @@ bool overlaps(const Range& a, const Range& b) {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// Whether the product of non-negative 32-bit extents stays below 2^31,
-// evaluated without overflow (each partial product is checked before the
-// next factor, so it never exceeds 2^62).
 bool below_2_31(std::initializer_list<int64_t> factors) {
   int64_t p = 1;
   for (const int64_t f : factors) {
@@ -67,20 +69,6 @@ bool below_2_31(std::initializer_list<int64_t> factors) {
   return true;
 }
 
-int check_dims(int32_t batch, int32_t seqlen, int32_t d_inner, int32_t d_state, int32_t d_conv) {
-  if (batch < 1 || seqlen < 1 || d_inner < 1 || d_state < 1)
-    return fail(MAMBA_ERR_SHAPE, "dims must be >= 1 (batch=%d seqlen=%d d_inner=%d d_state=%d)", batch,
-                seqlen, d_inner, d_state);
-  if (d_conv != 4) return fail(MAMBA_ERR_SHAPE, "d_conv must be 4 (got %d)", d_conv);
-  if (d_state != 8 && d_state != 16) return fail(MAMBA_ERR_SHAPE, "d_state must be 8 or 16 (got %d)", d_state);
-  const int64_t widest = d_inner > d_state ? d_inner : d_state;
-  if (!below_2_31({batch, seqlen, widest}) || !below_2_31({d_inner, d_state}))
-    return fail(MAMBA_ERR_SHAPE, "tensor too large (batch*seqlen*max(d_inner,d_state) must be < 2^31)");
-  return MAMBA_OK;
-}
-
-// Outputs may not overlap inputs, except that a state output may coincide
-// exactly with its own state input. Outputs may not overlap one another.
 int check_alias(const Range* ins, int n_in, const Range* outs, int n_out, const Range* pair_in,
                 const Range* pair_out, int n_pairs) {
   for (int o = 0; o < n_out; ++o) {
@@ -123,6 +111,25 @@ int check_device() {
     if (v == 2) return fail(MAMBA_ERR_DEVICE, "device %d is %s; this library is built for gfx950 only", dev, prop.gcnArchName);
   }
   if (v != 1) return fail(MAMBA_ERR_DEVICE, "current device is not gfx950; this library is built for gfx950 only");
+  return MAMBA_OK;
+}
+
+}  // namespace api
+}  // namespace mscan
+
+namespace {
+
+using namespace mscan::api;
+
+int check_dims(int32_t batch, int32_t seqlen, int32_t d_inner, int32_t d_state, int32_t d_conv) {
+  if (batch < 1 || seqlen < 1 || d_inner < 1 || d_state < 1)
+    return fail(MAMBA_ERR_SHAPE, "dims must be >= 1 (batch=%d seqlen=%d d_inner=%d d_state=%d)", batch,
+                seqlen, d_inner, d_state);
+  if (d_conv != 4) return fail(MAMBA_ERR_SHAPE, "d_conv must be 4 (got %d)", d_conv);
+  if (d_state != 8 && d_state != 16) return fail(MAMBA_ERR_SHAPE, "d_state must be 8 or 16 (got %d)", d_state);
+  const int64_t widest = d_inner > d_state ? d_inner : d_state;
+  if (!below_2_31({batch, seqlen, widest}) || !below_2_31({d_inner, d_state}))
+    return fail(MAMBA_ERR_SHAPE, "tensor too large (batch*seqlen*max(d_inner,d_state) must be < 2^31)");
   return MAMBA_OK;
 }
 
