@@ -1,0 +1,266 @@
+"""torch-tensor front end of linear attention with a decay for each head in
+libmamba_scan (`lin_attn_fwd`, its gradients `lin_attn_bwd`, and
+`lin_attn_step` for one token).
+
+Marshalling only: checks devices, dtypes and shapes, passes row strides where
+the library can read a tensor in place (columns of one projection's output) and
+makes others contiguous, allocates outputs and the workspace, and passes raw
+device addresses plus torch's current HIP stream to the entry points of
+include/mamba_linattn.h. The arithmetic is all in the library's kernels.
+"""
+import ctypes
+
+import torch
+
+from . import _binding as _b
+from .api import _IO, check_out, check_workspace
+
+EXPORTS = ("mamba_linattn_fwd_workspace_bytes", "mamba_linattn_fwd", "mamba_linattn_bwd_workspace_bytes",
+           "mamba_linattn_bwd", "mamba_linattn_step")
+_MAX_STRIDE = 1 << 24
+_F32 = torch.float32
+_lib = None
+
+
+def load():
+    """The scan library with the signatures of include/mamba_linattn.h declared."""
+    global _lib
+    if _lib is not None:
+        return _lib
+    lib = _b.load()
+    i32, i64, vp, sz, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float
+    rows = [vp, i64]
+    for name in ("mamba_linattn_fwd_workspace_bytes", "mamba_linattn_bwd_workspace_bytes"):
+        getattr(lib, name).restype = sz
+        getattr(lib, name).argtypes = [i32] * 7
+    lib.mamba_linattn_fwd.restype = ctypes.c_int
+    lib.mamba_linattn_fwd.argtypes = [i32] * 7 + [f32] + rows * 3 + [vp] * 6 + [sz, vp]
+    lib.mamba_linattn_bwd.restype = ctypes.c_int
+    lib.mamba_linattn_bwd.argtypes = [i32] * 7 + [f32] + rows * 3 + [vp] * 3 + rows + [vp] * 6 + [sz, vp]
+    lib.mamba_linattn_step.restype = ctypes.c_int
+    lib.mamba_linattn_step.argtypes = [i32] * 6 + [f32] + rows * 3 + [vp] * 5
+    _lib = lib
+    return lib
+
+
+def _tensor(t, name, dtype, device):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.device.type != "cuda":
+        raise _b.MambaScanError(7, "%s must be on the GPU (got %s); there is no CPU path" % (name, t.device))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s (got %s)" % (name, dtype, t.dtype))
+    if t.device != device:
+        raise _b.MambaScanError(7, "%s is on %s, expected %s" % (name, t.device, device))
+    return t
+
+
+def _io_of(x, name):
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if x.dtype not in _IO:
+        raise TypeError("io tensors must be float32 or bfloat16 (got %s)" % x.dtype)
+    return _IO[x.dtype]
+
+
+def row_stride(shape, strides, nrow):
+    """Elements between consecutive rows of a tensor whose first `nrow` dims number its rows and whose other
+    dims are one row's elements in order; 0 where the rows are not so laid out."""
+    want = 1
+    for n, s in zip(reversed(shape[nrow:]), reversed(strides[nrow:])):
+        if n != 1 and s != want:
+            return 0
+        want *= n
+    step = 0
+    count = 1
+    for n, s in zip(reversed(shape[:nrow]), reversed(strides[:nrow])):
+        if n != 1:
+            if step == 0:
+                step = s // count if s % count == 0 else 0
+                if step < want or step > _MAX_STRIDE:
+                    return 0
+            elif s != step * count:
+                return 0
+        count *= n
+    return step or want
+
+
+def _rows(t, name, dtype, device, nrow, align):
+    """(the tensor or a contiguous copy of it, its row stride), readable in place by the library."""
+    t = _tensor(t, name, dtype, device)
+    if t.is_contiguous():
+        if t.data_ptr() % align:
+            t = t.clone()
+        width = 1
+        for n in t.shape[nrow:]:
+            width *= n
+        return t, width
+    step = row_stride(t.shape, t.stride(), nrow)
+    if step and not t.data_ptr() % align and not step * t.element_size() % align:
+        return t, step
+    t = t.contiguous()
+    width = 1
+    for n in t.shape[nrow:]:
+        width *= n
+    return t, width
+
+
+def _f32(t, name, device, shape):
+    if t is None:
+        return None
+    t = _tensor(t, name, _F32, device)
+    if t.shape != shape:
+        raise _b.MambaScanError(2, "%s must be %s (got %s)" % (name, list(shape), list(t.shape)))
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+def _ids(seq_idx, device, batch, seqlen):
+    if seq_idx is None:
+        return None
+    if isinstance(seq_idx, torch.Tensor) and seq_idx.dtype in (torch.int64, torch.int16, torch.int8, torch.uint8):
+        seq_idx = seq_idx.to(torch.int32)
+    seq_idx = _tensor(seq_idx, "seq_idx", torch.int32, device)
+    if seq_idx.shape != (batch, seqlen):
+        raise _b.MambaScanError(2, "seq_idx must be [%d, %d]" % (batch, seqlen))
+    return seq_idx.contiguous()
+
+
+def _addr(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _check(lib, status, what):
+    if status != 0:
+        _b._check(lib, status, what)
+
+
+def launch(device, what, lib, fn, *args):
+    """Call an entry point with `device` current and its current stream as the last argument."""
+    if device.index == torch.cuda.current_device():
+        _check(lib, fn(*args, torch.cuda.current_stream(device).cuda_stream), what)
+    else:
+        with torch.cuda.device(device):
+            _check(lib, fn(*args, torch.cuda.current_stream(device).cuda_stream), what)
+
+
+def scratch(workspace, need, device):
+    """(address, bytes, tensor) of the caller's workspace or, where it is None, of a new one of `need` bytes."""
+    workspace = check_workspace(workspace, device)
+    if workspace is None:
+        if not need:
+            return 0, 0, None
+        workspace = torch.empty(need, device=device, dtype=torch.uint8)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _sizes(q, k, v, name_v="v"):
+    if q.dim() != 4 or v.dim() != 4:
+        raise _b.MambaScanError(2, "q and k must be [batch, seqlen, ngroups, d_k] and v [batch, seqlen, nheads, d_v]")
+    if k.shape != q.shape or v.shape[:2] != q.shape[:2]:
+        raise _b.MambaScanError(2, "shape mismatch between q %s, k %s and v %s" % (tuple(q.shape), tuple(k.shape),
+                                                                                 tuple(v.shape)))
+    batch, seqlen, ngroups, d_k = q.shape
+    return batch, seqlen, v.shape[2], ngroups, d_k, v.shape[3]
+
+
+def lin_attn_workspace_bytes(batch, seqlen, nheads, ngroups, d_k, d_v, dtype, backward=False):
+    """Bytes of workspace `lin_attn_fwd` (or, with `backward`, `lin_attn_bwd`) needs."""
+    lib = load()
+    fn = lib.mamba_linattn_bwd_workspace_bytes if backward else lib.mamba_linattn_fwd_workspace_bytes
+    return int(fn(batch, seqlen, nheads, ngroups, d_k, d_v, _IO[dtype]))
+
+
+def lin_attn_fwd(q, k, v, log_decay, state=None, *, scale=None, seq_idx=None, out=None, state_out=None,
+                 workspace=None, return_state=True):
+    """Whole sequence: q, k [batch, seqlen, ngroups, d_k]; v [batch, seqlen, nheads, d_v]; log_decay [nheads]
+    float32 (at most 0); state [batch, nheads, d_v, d_k] float32 or None (zeros); scale: a number, d_k ** -0.5 if
+    None; seq_idx [batch, seqlen] integer document ids or None (packed documents: the state restarts from zero
+    wherever the id changes). q, k and v may be columns of one wider tensor; they are read in place.
+    Returns (y like v, final state or None)."""
+    lib = load()
+    io = _io_of(q, "q")
+    dtype, dev = q.dtype, q.device
+    q, qs = _rows(q, "q", dtype, dev, 2, 16)
+    k, ks = _rows(k, "k", dtype, dev, 2, 16)
+    v, vs = _rows(v, "v", dtype, dev, 2, 16)
+    batch, seqlen, nheads, ngroups, d_k, d_v = sizes = _sizes(q, k, v)
+    log_decay = _f32(log_decay, "log_decay", dev, (nheads,))
+    state = _f32(state, "state", dev, (batch, nheads, d_v, d_k))
+    seq_idx = _ids(seq_idx, dev, batch, seqlen)
+    y = check_out(out, "out", v.shape, dtype, dev) if out is not None else torch.empty(v.shape, dtype=dtype, device=dev)
+    if state_out is not None:
+        check_out(state_out, "state_out", (batch, nheads, d_v, d_k), _F32, dev)
+    elif return_state:
+        state_out = torch.empty(batch, nheads, d_v, d_k, device=dev, dtype=_F32)
+    ws, ws_bytes, keep = scratch(workspace, lib.mamba_linattn_fwd_workspace_bytes(*sizes, io), dev)
+    launch(dev, "mamba_linattn_fwd", lib, lib.mamba_linattn_fwd, *sizes, io, d_k ** -0.5 if scale is None else scale,
+           q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _addr(seq_idx), _addr(log_decay), _addr(state),
+           y.data_ptr(), _addr(state_out), ws, ws_bytes)
+    return y, state_out
+
+
+def lin_attn_bwd(q, k, v, log_decay, dy, state=None, dstate=None, *, scale=None, seq_idx=None, workspace=None):
+    """Gradients of `lin_attn_fwd` given dy = dL/dy (like v) and dstate = dL/d(final state) ([batch, nheads, d_v, d_k]
+    float32, or None for zeros); the other arguments are the forward's.
+
+    Returns a dict: dq, dk, dv (dtype and shape of q, k, v; dq and dk are summed over the heads of a group) and,
+    where a state is given, dstate (float32, its gradient). The decays are constants: they get no gradient."""
+    lib = load()
+    io = _io_of(q, "q")
+    dtype, dev = q.dtype, q.device
+    q, qs = _rows(q, "q", dtype, dev, 2, 16)
+    k, ks = _rows(k, "k", dtype, dev, 2, 16)
+    v, vs = _rows(v, "v", dtype, dev, 2, 16)
+    dy, dys = _rows(dy, "dy", dtype, dev, 2, 16)
+    batch, seqlen, nheads, ngroups, d_k, d_v = sizes = _sizes(q, k, v)
+    if dy.shape != v.shape:
+        raise _b.MambaScanError(2, "dy must be %s (got %s)" % (list(v.shape), list(dy.shape)))
+    log_decay = _f32(log_decay, "log_decay", dev, (nheads,))
+    state = _f32(state, "state", dev, (batch, nheads, d_v, d_k))
+    dstate = _f32(dstate, "dstate", dev, (batch, nheads, d_v, d_k))
+    seq_idx = _ids(seq_idx, dev, batch, seqlen)
+    grads = {"dq": torch.empty(q.shape, dtype=dtype, device=dev), "dk": torch.empty(k.shape, dtype=dtype, device=dev),
+             "dv": torch.empty(v.shape, dtype=dtype, device=dev)}
+    if state is not None:
+        grads["dstate"] = torch.empty(state.shape, dtype=_F32, device=dev)
+    ws, ws_bytes, keep = scratch(workspace, lib.mamba_linattn_bwd_workspace_bytes(*sizes, io), dev)
+    launch(dev, "mamba_linattn_bwd", lib, lib.mamba_linattn_bwd, *sizes, io, d_k ** -0.5 if scale is None else scale,
+           q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _addr(seq_idx), _addr(log_decay), _addr(state),
+           dy.data_ptr(), dys, _addr(dstate), grads["dq"].data_ptr(), grads["dk"].data_ptr(), grads["dv"].data_ptr(),
+           _addr(grads.get("dstate")), ws, ws_bytes)
+    return grads
+
+
+def lin_attn_step(q, k, v, log_decay, state, *, scale=None, inplace=False, out=None):
+    """One token: q, k [batch, ngroups, d_k], v [batch, nheads, d_v], state [batch, nheads, d_v, d_k] float32
+    (required). Functional by default (a new state is returned); with inplace=True the given state is updated and
+    returned. Returns (y like v, state)."""
+    lib = load()
+    io = _io_of(q, "q")
+    dtype, dev = q.dtype, q.device
+    es = q.element_size()
+    q, qs = _rows(q, "q", dtype, dev, 1, es)
+    k, ks = _rows(k, "k", dtype, dev, 1, es)
+    v, vs = _rows(v, "v", dtype, dev, 1, es)
+    if state is None:
+        raise _b.MambaScanError(1, "lin_attn_step needs a state")
+    if q.dim() != 3 or v.dim() != 3:
+        raise _b.MambaScanError(2, "q and k must be [batch, ngroups, d_k] and v [batch, nheads, d_v]")
+    if k.shape != q.shape or v.shape[0] != q.shape[0]:
+        raise _b.MambaScanError(2, "shape mismatch between q %s, k %s and v %s" % (tuple(q.shape), tuple(k.shape),
+                                                                                 tuple(v.shape)))
+    batch, ngroups, d_k = q.shape
+    nheads, d_v = v.shape[1:]
+    log_decay = _f32(log_decay, "log_decay", dev, (nheads,))
+    if inplace:
+        check_out(state, "state", (batch, nheads, d_v, d_k), _F32, dev)
+        new = state
+    else:
+        state = _f32(state, "state", dev, (batch, nheads, d_v, d_k))
+        new = torch.empty(state.shape, dtype=_F32, device=dev)
+    y = check_out(out, "out", v.shape, dtype, dev) if out is not None else torch.empty(v.shape, dtype=dtype, device=dev)
+    launch(dev, "mamba_linattn_step", lib, lib.mamba_linattn_step, batch, nheads, ngroups, d_k, d_v, io,
+           d_k ** -0.5 if scale is None else scale, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+           _addr(log_decay), _addr(state), y.data_ptr(), _addr(new))
+    return y, new
