@@ -11,7 +11,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB_DIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIB_DIR, "libmamba_scan.so")
-SOURCES = ["mamba_scan_api.cpp", "linattn_api.cpp", "lin_attn.hip", "scan_fwd.hip", "scan_fwd_quad.hip", "scan_fwd_row.hip", "scan_step.hip",
+SOURCES = ["mamba_scan_api.cpp", "linattn_api.cpp", "lin_attn.hip", "gnorm_api.cpp", "group_norm.hip", "scan_fwd.hip", "scan_fwd_quad.hip", "scan_fwd_row.hip", "scan_step.hip",
            "scan_bwd.hip", "ssd.hip", "scan_noalloc.hip"]
 ARCH = "gfx950"
 
