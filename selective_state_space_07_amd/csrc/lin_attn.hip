@@ -22,8 +22,9 @@
 // to the last. A^T = K Q^T goes through LDS (each wave makes up to three of
 // the ten 16x16 tiles on and below the diagonal); y^T = V^T A^T + S Q^T and
 // S^T += K^T (w V) follow, V^T and K^T read transposed from row-major tiles.
-// The accumulators of S^T are the A operand of S Q^T when its K order is
-// permuted to match (slots 0-3: the first 16-row tile, slots 4-7: the second).
+// The rows of the S^T tiles are numbered (`spread`) so that the accumulators a
+// lane holds of two tiles are 8 consecutive k-elements: the A operand of S Q^T
+// as they stand.
 #include "linattn_internal.h"
 #include "mfma_frag.h"
 #include "scan_device.h"
@@ -51,31 +52,11 @@ __device__ __forceinline__ float power(float g2, int n) {
   return n == 0 ? 1.0f : exp2_hw(static_cast<float>(n) * g2);
 }
 
-// 8 k-values of a lane's column from a row-major tile [k][column]: rows
-// row0 + 8g .. + 7 of column col0 + (lane % 16).
-__device__ __forceinline__ Frag<1> frag_t(const uint16_t* tile, int pitch, int row0, int col0, int lane) {
-  typedef short s4 __attribute__((ext_vector_type(4)));
-  typedef __attribute__((address_space(3))) s4* lds_s4;
-  const int g = lane >> 4, i = lane & 15;
-  // a group of 16 lanes reads 4 rows of 16 columns and gets them transposed
-  const uint16_t* p = tile + (row0 + 8 * g + (i >> 2)) * pitch + col0 + (i & 3) * 4;
-  const s4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(p));
-  const s4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(p + 4 * pitch));
-  const u2 ua = __builtin_bit_cast(u2, a), ub = __builtin_bit_cast(u2, b);
-  const u4 v = {ua.x, ua.y, ub.x, ub.y};
-  return Frag<1>{__builtin_bit_cast(bf8, v)};
-}
-__device__ __forceinline__ Frag<0> frag_t(const float* tile, int pitch, int row0, int col0, int lane) {
-  const float* p = tile + (row0 + 8 * (lane >> 4)) * pitch + col0 + (lane & 15);
-  return Frag<0>{f4{p[0], p[pitch], p[2 * pitch], p[3 * pitch]},
-                 f4{p[4 * pitch], p[5 * pitch], p[6 * pitch], p[7 * pitch]}};
-}
-
 // Element j of a fragment as float32.
 __device__ __forceinline__ float frag_get(const Frag<1>& f, int j) { return static_cast<float>(f.v[j]); }
 __device__ __forceinline__ float frag_get(const Frag<0>& f, int j) { return j < 4 ? f.lo[j & 3] : f.hi[j & 3]; }
 
-// Zero the k-values below `first` (of this lane's eight).
+// Zero the k-values of a lane's eight that lie below `first`.
 __device__ __forceinline__ Frag<1> frag_from(const Frag<1>& f, int first) {
   u4 v = __builtin_bit_cast(u4, f.v);
 #pragma unroll
@@ -91,6 +72,22 @@ __device__ __forceinline__ Frag<0> frag_from(const Frag<0>& f, int first) {
     if (4 + j < first) r.hi[j] = 0.0f;
   }
   return r;
+}
+
+// The A operand of S Q^T from two neighbouring S^T tiles: 8 consecutive
+// k-elements, of which the first tile has the upper four where g is odd.
+template <int IO>
+__device__ __forceinline__ Frag<IO> state_frag(f4 even, f4 odd, int g);
+template <>
+__device__ __forceinline__ Frag<1> state_frag<1>(f4 even, f4 odd, int g) {
+  const u4 v = __builtin_bit_cast(u4, frag_regs<1>(even, odd).v);
+  const bool up = g & 1;
+  const u4 w = {up ? v.z : v.x, up ? v.w : v.y, up ? v.x : v.z, up ? v.y : v.w};
+  return Frag<1>{__builtin_bit_cast(bf8, w)};
+}
+template <>
+__device__ __forceinline__ Frag<0> state_frag<0>(f4 even, f4 odd, int g) {
+  return g & 1 ? Frag<0>{odd, even} : Frag<0>{even, odd};
 }
 
 // The weighted values w V as matrix-core operands. The state is kept and
@@ -131,30 +128,108 @@ struct Weighted<0> {
   __device__ __forceinline__ f4 mul(const Frag<0>& k, f4 c) const { return mma(k, part, c); }
 };
 
-// A 64-row tile on its way from global memory through registers into LDS (the
-// load is issued a chunk ahead). Rows from `rows` on and columns from `cols`
-// on are zero.
+// The column (of a tile, or of the state) that row or column m of a wave's i-th
+// 16-wide product stands for. Two neighbouring i share 32 columns: m / 4 = c
+// has columns 8 c .. 8 c + 3 of them in one and 8 c + 4 .. 8 c + 7 in the other,
+// the lower four first for even c (so that one transposed read takes both
+// halves of the 16-byte pieces, and with them all banks).
+__device__ __forceinline__ int spread(int i, int m) {
+  const int c = m >> 2;
+  return 32 * (i >> 1) + 8 * c + 4 * ((i ^ c) & 1) + (m & 3);
+}
+
+// A 64-row tile of W columns in LDS and its way there from global memory
+// through registers (the load is issued a chunk ahead).
+//
+// The 16-byte pieces of a row are exchanged by an exclusive-or with a number
+// made of the row's low bits, so that each way of reading hits every bank
+// once: 16 rows of one piece (operands with k along the row), and, in half a
+// wave of transposed reads, rows 0-3 and 8-11 of four half pieces.
+//
+// All reads are (base ^ constant) + constant with a base that depends on the
+// lane alone: a step along the row changes bits that the exchange leaves to
+// the exclusive-or, and 16 rows further the exchange is the same.
 template <int IO, int W>
 struct Tile {
   using T = typename Io<IO>::T;
-  static constexpr int kVec = 16 / static_cast<int>(sizeof(T));
-  static constexpr int kPitch = W + kVec;
-  static constexpr int kPer = W / kVec;
+  static constexpr uint32_t kRow = W * sizeof(T);  // bytes
+  static constexpr uint32_t kBytes = kC * kRow;
+  static constexpr int kPer = kRow / 16;
   static constexpr int kN = kC * kPer / kThreads;
   u4 v[kN];
-  __device__ __forceinline__ void load(const T* p, int64_t step, int rows, int cols, int tid) {
+
+  static __device__ __forceinline__ uint32_t exchange(int row) {
+    // 8 pieces a row: two rows span the banks, so the row's lowest bit is left
+    // out; else its low four bits, the middle two swapped
+    return kPer == 8 ? (row >> 1) & 7 : (row & 9) | ((row & 2) << 1) | ((row & 4) >> 1);
+  }
+  static __device__ __forceinline__ uint32_t at(int row, int byte) {
+    return static_cast<uint32_t>(row) * kRow + (static_cast<uint32_t>(byte) ^ (exchange(row) << 4));
+  }
+  // Rows 0 .. n - 1 of the chunk, row r at p + r * step (step in bytes, of either
+  // sign); rows from n on and columns from `cols` on are zero: the buffer
+  // range's answer to an offset out of range.
+  __device__ __forceinline__ void load(const void* p, int64_t step, int n, int cols, int tid) {
+    const uint32_t stride = static_cast<uint32_t>(step < 0 ? -step : step), width = min(cols, W) * sizeof(T);
+    const char* low = static_cast<const char*>(p) + (step < 0 ? step * (n - 1) : 0);
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(low), 0,
+                                                        stride * static_cast<uint32_t>(n - 1) + width, 0x00020000);
+    // a thread's pieces lie in one column, kThreads / kPer rows apart
+    asm volatile("" : "+v"(tid));  // the offsets are cheaper made again than kept over the loop
+    const uint32_t c = static_cast<uint32_t>(tid % kPer) * 16;
 #pragma unroll
     for (int q = 0; q < kN; ++q) {
-      const int i = tid + q * kThreads, r = i / kPer, c = (i - r * kPer) * kVec;
-      v[q] = u4{0u, 0u, 0u, 0u};
-      if (r < rows && c < cols) v[q] = *reinterpret_cast<const u4*>(p + r * step + c);
+      const int r = tid / kPer + q * (kThreads / kPer);
+      const uint32_t off = static_cast<uint32_t>(step < 0 ? n - 1 - r : r) * stride + c;
+      v[q] = __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, r < n && c < width ? off : 0xFFFFFFF0u, 0, 0));
     }
   }
-  __device__ __forceinline__ void store(T* lds, int tid) const {
+  __device__ __forceinline__ void store(char* lds, int tid) const {
 #pragma unroll
     for (int q = 0; q < kN; ++q) {
-      const int i = tid + q * kThreads, r = i / kPer, c = (i - r * kPer) * kVec;
-      *reinterpret_cast<u4*>(lds + r * kPitch + c) = v[q];
+      const int i = tid + q * kThreads, r = i / kPer;
+      *reinterpret_cast<u4*>(lds + at(r, (i - r * kPer) * 16)) = v[q];
+    }
+  }
+
+  // Row-major operands, k-values 32 kb + 8 g .. of row 16 i + l15.
+  static __device__ __forceinline__ uint32_t row_base(int l15, int g) { return at(l15, 8 * g * sizeof(T)); }
+  static __device__ __forceinline__ Frag<IO> row(const char* lds, uint32_t base, int i, int kb) {
+    const char* p = lds + 16 * i * kRow;
+    const uint32_t a = base ^ (32 * kb * sizeof(T));
+    if constexpr (IO == 1) {
+      return Frag<1>{__builtin_bit_cast(bf8, *reinterpret_cast<const u4*>(p + a))};
+    } else {
+      return Frag<0>{*reinterpret_cast<const f4*>(p + a), *reinterpret_cast<const f4*>(p + (a ^ 16))};
+    }
+  }
+  // Transposed operands: k runs over the tile's rows 32 kb + 8 g .., and lane
+  // l15 has column spread(i, l15).
+  static __device__ __forceinline__ uint32_t col_base(int l15, int g) {
+    // bfloat16: a group of 16 lanes reads 4 columns of 4 rows each and gets
+    // them transposed: lane l15 fetches row l15 / 4 of the columns of lanes 4 (l15 % 4) ..
+    if constexpr (IO == 1) return at(8 * g + (l15 >> 2), spread(0, 4 * (l15 & 3)) * 2);
+    return at(8 * g, spread(0, l15) * 4);
+  }
+  static __device__ __forceinline__ Frag<IO> col(const char* lds, uint32_t base, int i, int kb) {
+    const uint32_t a = base ^ (((i >> 1) * 32 + (i & 1) * 4) * sizeof(T));  // spread(i, .) is spread(0, .) ^ this
+    const char* p = lds + 32 * kb * kRow;
+    if constexpr (IO == 1) {
+      typedef short s4 __attribute__((ext_vector_type(4)));
+      typedef __attribute__((address_space(3))) s4* lds_s4;
+      const uint32_t x4 = (exchange(4) << 4);  // rows 4 to 7 of the eight
+      const u2 lo = __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(p + a)));
+      const u2 hi = __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(p + 4 * kRow + (a ^ x4))));
+      const u4 v = {lo.x, lo.y, hi.x, hi.y};
+      return Frag<1>{__builtin_bit_cast(bf8, v)};
+    } else {
+      Frag<0> f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f.lo[j] = *reinterpret_cast<const float*>(p + j * kRow + (a ^ (exchange(j) << 4)));
+        f.hi[j] = *reinterpret_cast<const float*>(p + (4 + j) * kRow + (a ^ (exchange(4 + j) << 4)));
+      }
+      return f;
     }
   }
 };
@@ -191,39 +266,49 @@ __device__ __forceinline__ int64_t ws_base(const LaArgs& a, const Place& p, int 
 
 // STATE: only the sum that a segment adds to the state (segments 0 .. nseg - 2).
 template <int IO, int KD, bool SEQ, bool STATE>
-__global__ __launch_bounds__(kThreads) void la_kernel(const LaArgs a) {
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 1 ? 3 : KD == 64 ? 2 : 1))) void la_kernel(
+    const LaArgs a) {
   using T = typename Io<IO>::T;
   using TileK = Tile<IO, KD>;
   using TileV = Tile<IO, kVS>;
+  using TileA = Tile<IO, kC>;
   constexpr int kTiles = KD / 16, kKb = KD / 32;
-  constexpr int kPK = TileK::kPitch, kPV = TileV::kPitch;
-  __shared__ T Ks[kC * kPK];
-  __shared__ T Vs[kC * kPV];
-  __shared__ T Qs[STATE ? 1 : kC * kPK];
-  __shared__ T As[STATE ? 1 : kC * kPV];
+  __shared__ __attribute__((aligned(512))) char lds[(STATE ? 1 : 2) * TileK::kBytes + (STATE ? 1 : 2) * TileV::kBytes];
+  char* const Ks = lds;
+  char* const Vs = lds + TileK::kBytes;
+  char* const As = Vs + TileV::kBytes;  // [t][s]
+  char* const Qs = As + TileA::kBytes;
 
   const Place pl = place(a, STATE ? a.nseg - 1 : a.nseg);
   if (!pl.live) return;
   const LaRole& R = a.role[pl.role];
-  const int kd = R.kd, vd = R.vd, v0 = pl.slice * kVS;
+  int kd = R.kd, vd = R.vd;
+  const int v0 = pl.slice * kVS;
   if (v0 >= vd) return;
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, l15 = lane & 15, g = lane >> 4;
+  // kept in scalar registers, not loaded again in the loop
+  float sc_out = R.sc_out, sc_kv = R.sc_kv;
+  void* out_p = R.out;
+  int es_out = IO == 0 || R.out_f32 ? 4 : 2, off = R.off, rev_i = R.rev, nheads = a.nheads, seqlen = a.seqlen;
+  asm volatile("" : "+s"(sc_out), "+s"(sc_kv), "+s"(out_p), "+s"(es_out), "+s"(off), "+s"(rev_i), "+s"(nheads),
+               "+s"(seqlen), "+s"(kd), "+s"(vd));
+  const bool rev = rev_i != 0;
+  const int tid = threadIdx.x, lane = tid & 63, l15_ = lane & 15, g_ = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rep = a.nheads / a.ngroups, grp = pl.h / rep;
   const int nchunks = (a.seqlen + kC - 1) / kC;
   const int c0 = pl.seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, nchunks);
-  const float g2 = a.log_decay[pl.h] * kLog2e;
-  const bool rev = R.rev;
-  const int off = R.off;
+  const float g2_ = a.log_decay[pl.h] * kLog2e;
   const int64_t row0 = static_cast<int64_t>(pl.b) * a.seqlen;
 
   const int64_t first = row0 + (rev ? a.seqlen - 1 : 0);
-  const int64_t qs = rev ? -R.q.row : R.q.row, ks = rev ? -R.k.row : R.k.row, vs = rev ? -R.v.row : R.v.row;
+  const int64_t es = rev ? -static_cast<int64_t>(sizeof(T)) : static_cast<int64_t>(sizeof(T));
+  const int64_t qs = R.q.row * es, ks = R.k.row * es, vs = R.v.row * es;  // bytes from a token to the next one
   const T* qp = static_cast<const T*>(R.q.p) + first * R.q.row + static_cast<int64_t>(R.q.per_group ? grp : pl.h) * kd;
   const T* kp = static_cast<const T*>(R.k.p) + first * R.k.row + static_cast<int64_t>(R.k.per_group ? grp : pl.h) * kd;
   const T* vp = static_cast<const T*>(R.v.p) + first * R.v.row + static_cast<int64_t>(R.v.per_group ? grp : pl.h) * vd + v0;
 
-  // the state of this lane: column v0 + 16 wv + l15, k-elements 16 i + 4 g + r
-  const int col = v0 + 16 * wv + l15;
+  // the state of this lane: column v0 + spread(wv, l15), k-elements spread(i, 4 g) + r
+  const int col = v0 + spread(wv, l15_);
   f4 S[kTiles];
 #pragma unroll
   for (int i = 0; i < kTiles; ++i) S[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -238,7 +323,7 @@ __global__ __launch_bounds__(kThreads) void la_kernel(const LaArgs a) {
       const float* st = R.state_in + (static_cast<int64_t>(pl.b) * a.nheads + pl.h) * vd * kd;
 #pragma unroll
       for (int i = 0; i < kTiles; ++i) {
-        const int e = 16 * i + 4 * g;
+        const int e = spread(i, 4 * g_);
         if (e >= kd) continue;
         if (R.state_t) {
 #pragma unroll
@@ -251,7 +336,7 @@ __global__ __launch_bounds__(kThreads) void la_kernel(const LaArgs a) {
     // the two 16x16 tiles above the diagonal that the products read
     for (int i = tid; i < 512; i += kThreads) {
       const int t = i >> 8, r = (i >> 4) & 15, c = i & 15;
-      Io<IO>::store(&As[(32 * t + r) * kPV + 32 * t + 16 + c], 0.0f);
+      Io<IO>::store(reinterpret_cast<T*>(As + TileA::at(32 * t + r, (32 * t + 16 + c) * sizeof(T))), 0.0f);
     }
   }
 
@@ -260,14 +345,17 @@ __global__ __launch_bounds__(kThreads) void la_kernel(const LaArgs a) {
   int id_own = 0, id_prev = 0;
   bool seen = false;  // a document began in this segment
   auto fetch = [&](int c) {
-    const int rows = min(kC, a.seqlen - c * kC);
-    kt.load(kp + static_cast<int64_t>(c) * kC * ks, ks, rows, kd, tid);
-    vt.load(vp + static_cast<int64_t>(c) * kC * vs, vs, rows, vd - v0, tid);
-    if (!STATE) qt.load(qp + static_cast<int64_t>(c) * kC * qs, qs, rows, kd, tid);
+    const int rows = min(kC, seqlen - c * kC);
+    auto from = [&](const T* p, int64_t step) {
+      return reinterpret_cast<const T*>(reinterpret_cast<const char*>(p) + static_cast<int64_t>(c) * kC * step);
+    };
+    kt.load(from(kp, ks), ks, rows, kd, tid);
+    vt.load(from(vp, vs), vs, rows, vd - v0, tid);
+    if (!STATE) qt.load(from(qp, qs), qs, rows, kd, tid);
     if (SEQ) {
       const int pos = c * kC + lane;
       id_own = id_prev = 0;
-      if (pos < a.seqlen && pos > 0) {
+      if (pos < seqlen && pos > 0) {
         id_own = a.seq_idx[first + (rev ? -pos : pos)];
         id_prev = a.seq_idx[first + (rev ? 1 - pos : pos - 1)];
       }
@@ -275,8 +363,16 @@ __global__ __launch_bounds__(kThreads) void la_kernel(const LaArgs a) {
   };
   fetch(c0);
 
+  const uint32_t row_b = TileK::row_base(l15_, g_), col_b = TileK::col_base(l15_, g_);
+  const uint32_t a_b = TileA::row_base(l15_, g_), v_b = TileV::col_base(l15_, g_);
   for (int c = c0; c < c1; ++c) {
-    const int n = min(kC, a.seqlen - c * kC);
+    // Renewed in each chunk: the addresses and weights that follow from these
+    // would otherwise all be kept in registers over the whole loop.
+    uint32_t at_row = row_b, at_col = col_b, at_a = a_b, at_v = v_b;
+    int l15 = l15_, g = g_;
+    float g2 = g2_;
+    asm volatile("" : "+v"(at_row), "+v"(at_col), "+v"(at_a), "+v"(at_v), "+v"(l15), "+v"(g), "+v"(g2));
+    const int n = min(kC, seqlen - c * kC);
     kt.store(Ks, tid);
     vt.store(Vs, tid);
     if (!STATE) qt.store(Qs, tid);
@@ -289,13 +385,13 @@ __global__ __launch_bounds__(kThreads) void la_kernel(const LaArgs a) {
 
     if (!STATE) {
       // A^T: rows s, columns t; each lane 4 rows s of one column t
+#pragma unroll 1
       for (int idx = wv; idx < 10; idx += 4) {
         const int j = idx < 1 ? 0 : idx < 3 ? 1 : idx < 6 ? 2 : 3, i = idx - j * (j + 1) / 2;
         f4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int kb = 0; kb < kKb; ++kb)
-          acc = mma(frag8(Ks + (16 * i + l15) * kPK + 32 * kb + 8 * g),
-                    frag8(Qs + (16 * j + l15) * kPK + 32 * kb + 8 * g), acc);
+          acc = mma(TileK::row(Ks, at_row, i, kb), TileK::row(Qs, at_row, j, kb), acc);
         const int t = 16 * j + l15, s = 16 * i + 4 * g;
         int from = 0;
         if (SEQ) {
@@ -304,8 +400,8 @@ __global__ __launch_bounds__(kThreads) void la_kernel(const LaArgs a) {
         }
 #pragma unroll
         for (int r = 0; r < 4; ++r)  // chosen, not multiplied, so that masked pairs drop infinities and NaN
-          acc[r] = s + r <= t && s + r >= from ? acc[r] * (power(g2, t - s - r) * (R.sc_out * R.sc_kv)) : 0.0f;
-        T* dst = As + t * kPV + s;
+          acc[r] = s + r <= t && s + r >= from ? acc[r] * (power(g2, t - s - r) * (sc_out * sc_kv)) : 0.0f;
+        char* dst = As + 16 * j * TileA::kRow + (TileA::at(l15, 4 * g * sizeof(T)) ^ (16 * i * sizeof(T)));  // row t, from column s
         if (IO == 1) {
           typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
           const bf4 v = {static_cast<__bf16>(acc[0]), static_cast<__bf16>(acc[1]), static_cast<__bf16>(acc[2]),
@@ -320,23 +416,20 @@ __global__ __launch_bounds__(kThreads) void la_kernel(const LaArgs a) {
 
     Frag<IO> vf[2];
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) vf[kb] = frag_t(Vs, kPV, 32 * kb, 16 * wv, lane);
+    for (int kb = 0; kb < 2; ++kb) vf[kb] = TileV::col(Vs, at_v, wv, kb);
 
     if (!STATE) {
       f4 y[4];
+      // the state's part, lam^(t + off) S q_t; `from[j]`: where token t's document begins in the chunk
       int from[4];
-#pragma unroll 1
-      for (int pass = 0; pass < 2; ++pass) {
+      auto carried = [&](uint32_t at) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) y[j] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int kb = 0; kb < kKb; ++kb) {
-          const Frag<IO> sf = frag_regs<IO>(S[2 * kb], S[2 * kb + 1]);
+          const Frag<IO> sf = state_frag<IO>(S[2 * kb], S[2 * kb + 1], g);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const T* q = Qs + (16 * j + l15) * kPK + 32 * kb + 4 * g;
-            y[j] = mma(sf, frag44(q, q + 16), y[j]);
-          }
+          for (int j = 0; j < 4; ++j) y[j] = mma(sf, TileK::row(Qs, at, j, kb), y[j]);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -348,80 +441,85 @@ __global__ __launch_bounds__(kThreads) void la_kernel(const LaArgs a) {
             from[j] = m ? 63 - __builtin_clzll(m) : 0;
             open = m == 0;
           }
-          const float w = power(g2, t + off) * R.sc_out;
+          const float w = power(g2, t + off) * sc_out;
 #pragma unroll
           for (int r = 0; r < 4; ++r) y[j][r] = open ? y[j][r] * w : 0.0f;
         }
-        if (pass == 0) {
-          float bad = 0.0f;
+      };
+      carried(at_row);
+      float bad = 0.0f;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const T* p = As + (16 * j + l15) * kPV + 8 * g;
-            y[j] = mma(vf[0], frag8(p), y[j]);
-            if (j >= 2) y[j] = mma(vf[1], frag8(p + 32), y[j]);
+      for (int j = 0; j < 4; ++j) {
+        y[j] = mma(vf[0], TileA::row(As, at_a, j, 0), y[j]);
+        if (j >= 2) y[j] = mma(vf[1], TileA::row(As, at_a, j, 1), y[j]);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) bad = fmaf(y[j][r], 0.0f, bad);
-          }
-          // An infinity or NaN in v also reaches the tokens that it is masked
-          // for, as 0 * inf. Where any sum is not finite the second pass takes
-          // the sums again, over the unmasked tokens alone.
-          if (!__any(bad != 0.0f)) break;
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int t = 16 * j + l15;
-            for (int s = 0; s < kC; ++s) {
-              if (s > t || s < from[j]) continue;
-              const float p = Io<IO>::cvt(As[t * kPV + s]);
-#pragma unroll
-              for (int r = 0; r < 4; ++r) y[j][r] = fmaf(p, Io<IO>::cvt(Vs[s * kPV + 16 * wv + 4 * g + r]), y[j][r]);
-            }
-          }
-        }
+        for (int r = 0; r < 4; ++r) bad = fmaf(y[j][r], 0.0f, bad);
       }
-      // each lane holds 4 consecutive columns of one token
-      const int oc = v0 + 16 * wv + 4 * g;
-      if (oc < vd) {
+      // An infinity or NaN in v also reaches the tokens that it is masked for,
+      // as 0 * inf. Where any sum is not finite the sums are taken again, over
+      // the unmasked tokens alone.
+      if (__any(bad != 0.0f)) {
+        uint32_t again = at_row;
+        asm volatile("" : "+v"(again));  // read again, not kept from above
+        carried(again);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int t = 16 * j + l15;
-          if (t >= n) continue;
-          const int64_t tok = first + (rev ? -static_cast<int64_t>(c * kC + t) : c * kC + t);
-          const int64_t o = (tok * a.nheads + pl.h) * vd + oc;
-          if (IO == 0 || R.out_f32) {
-            *reinterpret_cast<f4*>(static_cast<float*>(R.out) + o) = y[j];
-          } else {
-            typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
-            const bf4 v = {static_cast<__bf16>(y[j][0]), static_cast<__bf16>(y[j][1]), static_cast<__bf16>(y[j][2]),
-                           static_cast<__bf16>(y[j][3])};
-            *reinterpret_cast<u2*>(static_cast<uint16_t*>(R.out) + o) = __builtin_bit_cast(u2, v);
+#pragma unroll 1
+          for (int s = 0; s < kC; ++s) {
+            if (s > t || s < from[j]) continue;
+            const float p = Io<IO>::load(reinterpret_cast<const T*>(As + TileA::at(t, s * sizeof(T))));
+            const T* v = reinterpret_cast<const T*>(Vs + TileV::at(s, spread(wv, 4 * g) * sizeof(T)));
+#pragma unroll
+            for (int r = 0; r < 4; ++r) y[j][r] = fmaf(p, Io<IO>::load(v + r), y[j][r]);
           }
+        }
+      }
+      // each lane holds 4 consecutive columns of one token; rows from n on and
+      // columns from vd on are out of the buffer's range and dropped
+      const int oc = spread(wv, 4 * g);
+      const uint32_t row_out = static_cast<uint32_t>(nheads) * vd * es_out;
+      const int64_t low = first + (rev ? -static_cast<int64_t>(c * kC + n - 1) : c * kC);
+      char* const out = static_cast<char*>(out_p) + ((low * nheads + pl.h) * vd + v0) * es_out;
+      const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(out, 0, row_out * (n - 1) + (vd - v0) * es_out, 0x00020000);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int t = 16 * j + l15;
+        const uint32_t o = t < n && oc < vd - v0
+                               ? static_cast<uint32_t>(rev ? n - 1 - t : t) * row_out + static_cast<uint32_t>(oc) * es_out
+                               : 0xFFFFFFF0u;
+        if (IO == 0 || es_out == 4) {
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, y[j]), rsrc, o, 0, 0);
+        } else {
+          typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
+          const bf4 v = {static_cast<__bf16>(y[j][0]), static_cast<__bf16>(y[j][1]), static_cast<__bf16>(y[j][2]),
+                         static_cast<__bf16>(y[j][3])};
+          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u2, v), rsrc, o, 0, 0);
         }
       }
     }
 
     // S^T = lam^n S^T + K^T (w V) over the tokens of the last document
-    Weighted<IO> wvf[2];
+    const float keep = power(g2, n);
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) S[i][r] = begins ? 0.0f : S[i][r] * keep;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
       float x[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int s = 32 * kb + 8 * g + j;
-        x[j] = s < n && s >= last ? frag_get(vf[kb], j) * (power(g2, n - off - s) * R.sc_kv) : 0.0f;
+        x[j] = s < n && s >= last ? frag_get(vf[kb], j) * (power(g2, n - off - s) * sc_kv) : 0.0f;
       }
-      wvf[kb].set(x);
-    }
-    const float keep = power(g2, n);
+      Weighted<IO> wvf;
+      wvf.set(x);
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) S[i][r] = begins ? 0.0f : S[i][r] * keep;
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        Frag<IO> kf = frag_t(Ks, kPK, 32 * kb, 16 * i, lane);
+      for (int i = 0; i < kTiles; ++i) {
+        Frag<IO> kf = TileK::col(Ks, at_col, i, kb);
         if (SEQ) kf = frag_from(kf, last - (32 * kb + 8 * g));
-        S[i] = wvf[kb].mul(kf, S[i]);
+        S[i] = wvf.mul(kf, S[i]);
       }
     }
     __syncthreads();
@@ -439,7 +537,7 @@ __global__ __launch_bounds__(kThreads) void la_kernel(const LaArgs a) {
     float* st = R.state_out + (static_cast<int64_t>(pl.b) * a.nheads + pl.h) * vd * kd + static_cast<int64_t>(col) * kd;
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) {
-      const int e = 16 * i + 4 * g;
+      const int e = spread(i, 4 * g_);
       if (e < kd) *reinterpret_cast<f4*>(st + e) = S[i];
     }
   }
@@ -463,7 +561,7 @@ __global__ __launch_bounds__(kThreads) void la_join_kernel(const LaArgs a) {
   const LaRole& R = a.role[p.role];
   if (p.slice * kVS >= R.vd) return;
   const int tid = threadIdx.x, lane = tid & 63;
-  const int col = p.slice * kVS + 16 * (tid >> 6) + (lane & 15), e = 16 * i + 4 * (lane >> 4);
+  const int col = p.slice * kVS + spread(tid >> 6, lane & 15), e = spread(i, 4 * (lane >> 4));
   f4 s = {0.0f, 0.0f, 0.0f, 0.0f};
   if (R.state_in && col < R.vd && e < R.kd) {
     const float* st = R.state_in + (static_cast<int64_t>(p.b) * a.nheads + p.h) * R.vd * R.kd;
