@@ -92,40 +92,47 @@ __device__ __forceinline__ Frag<0> state_frag<0>(f4 even, f4 odd, int g) {
 
 // The weighted values w V as matrix-core operands. The state is kept and
 // returned in float32, so for bfloat16 io the products w v (24 significant
-// bits) are split into three bfloat16 parts of 8 bits each (the remainder is
-// below 2^-24) and multiplied three times: a single rounding would leave the
-// state with 8 bits.
+// bits) are split into bfloat16 parts, each the rounded rest of those before
+// it, and multiplied once for each: three parts hold all 24 bits. Where the
+// state is not returned, only y sees it, rounded to bfloat16 itself, and two
+// parts (16 bits) do; one would double the rounding that y gets.
 template <int IO>
 struct Weighted;
 template <>
 struct Weighted<1> {
+  static constexpr int kParts = 3;
   Frag<1> part[3];
-  __device__ __forceinline__ void set(const float (&x)[8]) {
-    float r[8];
+  __device__ __forceinline__ void set(const float (&x)[8], bool three) {
+    float r[8], bad = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) r[j] = x[j];
+    for (int j = 0; j < 8; ++j) {
+      r[j] = x[j];
+      bad = fmaf(x[j], 0.0f, bad);
+    }
+    const bool inf = __any(bad != 0.0f);  // an infinity or NaN is whole in its first part
 #pragma unroll
     for (int p = 0; p < 3; ++p) {
+      if (p == 2 && !three) break;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const __bf16 h = static_cast<__bf16>(r[j]);
         part[p].v[j] = h;
-        const float rest = r[j] - static_cast<float>(h);
-        r[j] = rest == rest ? rest : 0.0f;  // an infinity is whole in its first part
+        r[j] -= static_cast<float>(h);
+      }
+      if (inf) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[j] = r[j] == r[j] ? r[j] : 0.0f;
       }
     }
-  }
-  __device__ __forceinline__ f4 mul(const Frag<1>& k, f4 c) const {
-    return mma(k, part[0], mma(k, part[1], mma(k, part[2], c)));
   }
 };
 template <>
 struct Weighted<0> {
-  Frag<0> part;
-  __device__ __forceinline__ void set(const float (&x)[8]) {
-    part = Frag<0>{f4{x[0], x[1], x[2], x[3]}, f4{x[4], x[5], x[6], x[7]}};
+  static constexpr int kParts = 1;
+  Frag<0> part[1];
+  __device__ __forceinline__ void set(const float (&x)[8], bool) {
+    part[0] = Frag<0>{f4{x[0], x[1], x[2], x[3]}, f4{x[4], x[5], x[6], x[7]}};
   }
-  __device__ __forceinline__ f4 mul(const Frag<0>& k, f4 c) const { return mma(k, part, c); }
 };
 
 // The column (of a tile, or of the state) that row or column m of a wave's i-th
@@ -278,6 +285,9 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 
   char* const Vs = lds + TileK::kBytes;
   char* const As = Vs + TileV::kBytes;  // [t][s]
   char* const Qs = As + TileA::kBytes;
+  // powers of lam with their factors: of a score at distance 63 - m (0 from 64 on, above the diagonal), of the
+  // state read at token t, of token s on its way into the state of a chunk of n
+  __shared__ float w_score[80], w_out[kC], w_in[kC];
 
   const Place pl = place(a, STATE ? a.nseg - 1 : a.nseg);
   if (!pl.live) return;
@@ -288,6 +298,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 
   // kept in scalar registers, not loaded again in the loop
   float sc_out = R.sc_out, sc_kv = R.sc_kv;
   void* out_p = R.out;
+  const bool three = R.state_out != nullptr;
   int es_out = IO == 0 || R.out_f32 ? 4 : 2, off = R.off, rev_i = R.rev, nheads = a.nheads, seqlen = a.seqlen;
   asm volatile("" : "+s"(sc_out), "+s"(sc_kv), "+s"(out_p), "+s"(es_out), "+s"(off), "+s"(rev_i), "+s"(nheads),
                "+s"(seqlen), "+s"(kd), "+s"(vd));
@@ -297,7 +308,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 
   const int rep = a.nheads / a.ngroups, grp = pl.h / rep;
   const int nchunks = (a.seqlen + kC - 1) / kC;
   const int c0 = pl.seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, nchunks);
-  const float g2_ = a.log_decay[pl.h] * kLog2e;
+  const float g2 = a.log_decay[pl.h] * kLog2e;
   const int64_t row0 = static_cast<int64_t>(pl.b) * a.seqlen;
 
   const int64_t first = row0 + (rev ? a.seqlen - 1 : 0);
@@ -340,6 +351,10 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 
     }
   }
 
+  if (!STATE && tid < 80) w_score[tid] = tid < kC ? power(g2, 63 - tid) * (sc_out * sc_kv) : 0.0f;
+  if (!STATE && tid < kC) w_out[tid] = power(g2, tid + off) * sc_out;
+  const float keep_full = power(g2, kC);
+
   TileK kt, qt;
   TileV vt;
   int id_own = 0, id_prev = 0;
@@ -366,16 +381,16 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 
   const uint32_t row_b = TileK::row_base(l15_, g_), col_b = TileK::col_base(l15_, g_);
   const uint32_t a_b = TileA::row_base(l15_, g_), v_b = TileV::col_base(l15_, g_);
   for (int c = c0; c < c1; ++c) {
-    // Renewed in each chunk: the addresses and weights that follow from these
-    // would otherwise all be kept in registers over the whole loop.
+    // Renewed in each chunk: the addresses that follow from these would
+    // otherwise all be kept in registers over the whole loop.
     uint32_t at_row = row_b, at_col = col_b, at_a = a_b, at_v = v_b;
     int l15 = l15_, g = g_;
-    float g2 = g2_;
-    asm volatile("" : "+v"(at_row), "+v"(at_col), "+v"(at_a), "+v"(at_v), "+v"(l15), "+v"(g), "+v"(g2));
+    asm volatile("" : "+v"(at_row), "+v"(at_col), "+v"(at_a), "+v"(at_v), "+v"(l15), "+v"(g));
     const int n = min(kC, seqlen - c * kC);
     kt.store(Ks, tid);
     vt.store(Vs, tid);
     if (!STATE) qt.store(Qs, tid);
+    if ((c == c0 || n < kC) && tid < kC) w_in[tid] = tid < n ? power(g2, n - off - tid) * sc_kv : 0.0f;
     // bit s: a document begins at token s of the chunk
     const uint64_t begins = SEQ ? __ballot(id_own != id_prev) : 0;
     const int last = begins ? 63 - __builtin_clzll(begins) : 0;  // the last document's first token
@@ -384,24 +399,38 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 
     if (c + 1 < c1) fetch(c + 1);
 
     if (!STATE) {
-      // A^T: rows s, columns t; each lane 4 rows s of one column t
+      // A^T: rows s, columns t; wave j has the 16 tokens t from 16 j on, and each lane 4 rows s of one column t
+      const int j = wv, t = 16 * j + l15;
+      int from = 0;
+      if (SEQ) {
+        const uint64_t m = begins & (~0ull >> (63 - t));
+        from = m ? 63 - __builtin_clzll(m) : 0;
+      }
+      const char* q_at = Qs + 16 * j * TileK::kRow;
+      char* a_at = As + 16 * j * TileA::kRow;
+      const uint32_t to = TileA::at(l15, 4 * g * sizeof(T));
+      Frag<IO> qf[kKb], kf[kKb];
+#pragma unroll
+      for (int kb = 0; kb < kKb; ++kb) {
+        kf[kb] = TileK::row(Ks, at_row, 0, kb);
+        qf[kb] = TileK::row(q_at, at_row, 0, kb);
+      }
 #pragma unroll 1
-      for (int idx = wv; idx < 10; idx += 4) {
-        const int j = idx < 1 ? 0 : idx < 3 ? 1 : idx < 6 ? 2 : 3, i = idx - j * (j + 1) / 2;
+      for (int i = 0; i <= j; ++i) {
         f4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int kb = 0; kb < kKb; ++kb)
-          acc = mma(TileK::row(Ks, at_row, i, kb), TileK::row(Qs, at_row, j, kb), acc);
-        const int t = 16 * j + l15, s = 16 * i + 4 * g;
-        int from = 0;
-        if (SEQ) {
-          const uint64_t m = begins & (~0ull >> (63 - t));
-          from = m ? 63 - __builtin_clzll(m) : 0;
+        for (int kb = 0; kb < kKb; ++kb) acc = mma(kf[kb], qf[kb], acc);
+        const int s = 16 * i + 4 * g;
+        const float* w = w_score + 63 - t + s;
+        const f4 wt = {w[0], w[1], w[2], w[3]};
+        if (i < j) {
+#pragma unroll
+          for (int kb = 0; kb < kKb; ++kb) kf[kb] = TileK::row(Ks + 16 * (i + 1) * TileK::kRow, at_row, 0, kb);
         }
 #pragma unroll
         for (int r = 0; r < 4; ++r)  // chosen, not multiplied, so that masked pairs drop infinities and NaN
-          acc[r] = s + r <= t && s + r >= from ? acc[r] * (power(g2, t - s - r) * (sc_out * sc_kv)) : 0.0f;
-        char* dst = As + 16 * j * TileA::kRow + (TileA::at(l15, 4 * g * sizeof(T)) ^ (16 * i * sizeof(T)));  // row t, from column s
+          acc[r] = s + r <= t && s + r >= from ? acc[r] * wt[r] : 0.0f;
+        char* dst = a_at + (to ^ (16 * i * sizeof(T)));  // row t, from column s
         if (IO == 1) {
           typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
           const bf4 v = {static_cast<__bf16>(acc[0]), static_cast<__bf16>(acc[1]), static_cast<__bf16>(acc[2]),
@@ -427,9 +456,12 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 
         for (int j = 0; j < 4; ++j) y[j] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int kb = 0; kb < kKb; ++kb) {
+          Frag<IO> qf[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) qf[j] = TileK::row(Qs, at, j, kb);
           const Frag<IO> sf = state_frag<IO>(S[2 * kb], S[2 * kb + 1], g);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) y[j] = mma(sf, TileK::row(Qs, at, j, kb), y[j]);
+          for (int j = 0; j < 4; ++j) y[j] = mma(sf, qf[j], y[j]);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -441,7 +473,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 
             from[j] = m ? 63 - __builtin_clzll(m) : 0;
             open = m == 0;
           }
-          const float w = power(g2, t + off) * sc_out;
+          const float w = w_out[t];
 #pragma unroll
           for (int r = 0; r < 4; ++r) y[j][r] = open ? y[j][r] * w : 0.0f;
         }
@@ -500,7 +532,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 
     }
 
     // S^T = lam^n S^T + K^T (w V) over the tokens of the last document
-    const float keep = power(g2, n);
+    const float keep = n == kC ? keep_full : power(g2, n);
 #pragma unroll
     for (int i = 0; i < kTiles; ++i)
 #pragma unroll
@@ -508,18 +540,30 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
       float x[8];
+      const f4 w[2] = {*reinterpret_cast<const f4*>(w_in + 32 * kb + 8 * g),
+                       *reinterpret_cast<const f4*>(w_in + 32 * kb + 8 * g + 4)};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int s = 32 * kb + 8 * g + j;
-        x[j] = s < n && s >= last ? frag_get(vf[kb], j) * (power(g2, n - off - s) * sc_kv) : 0.0f;
+        x[j] = frag_get(vf[kb], j) * w[j >> 2][j & 3];
+        if (SEQ) x[j] = 32 * kb + 8 * g + j >= last ? x[j] : 0.0f;
       }
       Weighted<IO> wvf;
-      wvf.set(x);
+      wvf.set(x, three);
+      // four tiles at a time: their operands first, then one product with each part in turn
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i) {
-        Frag<IO> kf = TileK::col(Ks, at_col, i, kb);
-        if (SEQ) kf = frag_from(kf, last - (32 * kb + 8 * g));
-        S[i] = wvf.mul(kf, S[i]);
+      for (int i0 = 0; i0 < kTiles; i0 += 4) {
+        Frag<IO> kf[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          kf[i] = TileK::col(Ks, at_col, i0 + i, kb);
+          if (SEQ) kf[i] = frag_from(kf[i], last - (32 * kb + 8 * g));
+        }
+#pragma unroll
+        for (int p = Weighted<IO>::kParts - 1; p >= 0; --p) {
+          if (p == 2 && !three) continue;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) S[i0 + i] = mma(kf[i], wvf.part[p], S[i0 + i]);
+        }
       }
     }
     __syncthreads();
