@@ -16,15 +16,19 @@
 // state) stands at its first token, not one step before it: `off` is 0 there,
 // in lam^(t+off) and lam^(64-off-s).
 //
-// A workgroup of four waves walks the chunks of one (batch row, head, 64
-// columns of v) in order. A wave keeps the state of its 16 columns in
-// accumulators, S^T tiles [16 k-elements x 16 columns], from the first chunk
-// to the last. A^T = K Q^T goes through LDS (each wave makes up to three of
-// the ten 16x16 tiles on and below the diagonal); y^T = V^T A^T + S Q^T and
-// S^T += K^T (w V) follow, V^T and K^T read transposed from row-major tiles.
-// The rows of the S^T tiles are numbered (`spread`) so that the accumulators a
-// lane holds of two tiles are 8 consecutive k-elements: the A operand of S Q^T
-// as they stand.
+// A workgroup walks the chunks of one (batch row, head, 64 columns of v) in
+// order, eight waves with two tasks. Four of them own 16 tokens of the chunk
+// each and make y: A^T = K Q^T (the scores, which stay in registers: the rows
+// of its 16x16 tiles are numbered, by `spread`, so that the accumulators of
+// two tiles are the next product's operand as they stand), then
+// y^T = S Q^T + V^T A^T. The other four own 16 columns of v each and keep the
+// state of theirs in accumulators, S^T += K^T (w V), from the first chunk to
+// the last; each chunk's starting state goes to the first four through LDS.
+// Both tasks of a chunk run at once, one wave of each on a SIMD, and with K, V
+// and S in LDS twice there is one barrier to a chunk. K and V come through
+// registers two chunks ahead, Q straight into the lanes that multiply it.
+#include <type_traits>
+
 #include "linattn_internal.h"
 #include "mfma_frag.h"
 #include "scan_device.h"
@@ -35,7 +39,7 @@ namespace {
 
 constexpr int kC = 64;         // tokens per chunk
 constexpr int kVS = 64;        // columns of v per workgroup
-constexpr int kThreads = 256;  // four waves of 16 columns
+constexpr int kThreads = 256;  // four waves of 16 columns: the state's task
 constexpr int kMaxRoles = 3;
 
 struct LaArgs {
@@ -145,65 +149,80 @@ __device__ __forceinline__ int spread(int i, int m) {
   return 32 * (i >> 1) + 8 * c + 4 * ((i ^ c) & 1) + (m & 3);
 }
 
+// `off` where ok, else an offset beyond any buffer range. Without a branch:
+// the compiler would put the load or store behind it.
+__device__ __forceinline__ uint32_t in_range(uint32_t off, bool ok) {
+  return off | ((static_cast<uint32_t>(ok) - 1u) & 0xFFFFFFC0u);
+}
+// The place of row r in memory of n rows that lie upwards, or downwards.
+struct Order {
+  int base, sign;
+  __device__ __forceinline__ Order(bool rev, int n) : base(rev ? n - 1 : 0), sign(rev ? -1 : 1) {}
+  __device__ __forceinline__ uint32_t operator()(int r) const { return static_cast<uint32_t>(base + sign * r); }
+};
+
 // A 64-row tile of W columns in LDS and its way there from global memory
 // through registers (the load is issued a chunk ahead).
 //
 // The 16-byte pieces of a row are exchanged by an exclusive-or with a number
 // made of the row's low bits, so that each way of reading hits every bank
-// once: 16 rows of one piece (operands with k along the row), and, in half a
-// wave of transposed reads, rows 0-3 and 8-11 of four half pieces.
+// once: one piece of the 16 rows spread(i, .), and, in half a wave of
+// transposed reads, rows 0-3 and 8-11 of four half pieces.
 //
 // All reads are (base ^ constant) + constant with a base that depends on the
 // lane alone: a step along the row changes bits that the exchange leaves to
-// the exclusive-or, and 16 rows further the exchange is the same.
-template <int IO, int W>
+// the exclusive-or, and 4 or 32 rows further the exchange is the same.
+template <int IO, int W, int NT>
 struct Tile {
   using T = typename Io<IO>::T;
   static constexpr uint32_t kRow = W * sizeof(T);  // bytes
   static constexpr uint32_t kBytes = kC * kRow;
   static constexpr int kPer = kRow / 16;
-  static constexpr int kN = kC * kPer / kThreads;
+  static constexpr int kN = kC * kPer / NT;  // pieces of a thread
   u4 v[kN];
 
   static __device__ __forceinline__ uint32_t exchange(int row) {
     // 8 pieces a row: two rows span the banks, so the row's lowest bit is left
-    // out; else its low four bits, the middle two swapped
-    return kPer == 8 ? (row >> 1) & 7 : (row & 9) | ((row & 2) << 1) | ((row & 4) >> 1);
+    // out; bit 2 is, for its rows are read apart; bits 1 and 3 must not meet
+    // in bit 1, which tells the half pieces of one transposed read apart
+    const int x = ((row >> 1) & 1) | ((row >> 3) & 2) | ((row >> 1) & 4);  // row bits 1, 4, 3
+    return kPer == 8 ? x : ((x & 1) << 2) | (x & 2) | ((x & 4) << 1) | (row & 1);
   }
   static __device__ __forceinline__ uint32_t at(int row, int byte) {
     return static_cast<uint32_t>(row) * kRow + (static_cast<uint32_t>(byte) ^ (exchange(row) << 4));
   }
   // Rows 0 .. n - 1 of the chunk, row r at p + r * step (step in bytes, of either
   // sign); rows from n on and columns from `cols` on are zero: the buffer
-  // range's answer to an offset out of range.
-  __device__ __forceinline__ void load(const void* p, int64_t step, int n, int cols, int tid) {
+  // range's answer to an offset out of range. With n <= 0 nothing is read, and
+  // no branch stands around a load: behind one the compiler could not tell the
+  // loads in flight apart and would wait for all of them.
+  __device__ __forceinline__ void load(const void* p, int64_t step, int n, int cols, uint32_t tid) {
     const uint32_t stride = static_cast<uint32_t>(step < 0 ? -step : step), width = min(cols, W) * sizeof(T);
-    const char* low = static_cast<const char*>(p) + (step < 0 ? step * (n - 1) : 0);
-    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(low), 0,
-                                                        stride * static_cast<uint32_t>(n - 1) + width, 0x00020000);
-    // a thread's pieces lie in one column, kThreads / kPer rows apart
+    const Order order(step < 0, n);
+    const char* low = static_cast<const char*>(p) + step * order.base;
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(low), 0, n > 0 ? stride * static_cast<uint32_t>(n - 1) + width : 0, 0x00020000);
+    // a thread's pieces lie in one column, NT / kPer rows apart
     asm volatile("" : "+v"(tid));  // the offsets are cheaper made again than kept over the loop
-    const uint32_t c = static_cast<uint32_t>(tid % kPer) * 16;
+    const uint32_t c = tid % kPer * 16;
 #pragma unroll
     for (int q = 0; q < kN; ++q) {
-      const int r = tid / kPer + q * (kThreads / kPer);
-      const uint32_t off = static_cast<uint32_t>(step < 0 ? n - 1 - r : r) * stride + c;
-      v[q] = __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, r < n && c < width ? off : 0xFFFFFFF0u, 0, 0));
+      const int r = static_cast<int>(tid / kPer) + q * (NT / kPer);
+      const uint32_t off = in_range(order(r) * stride + c, (r < n) & (c < width));
+      v[q] = __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, off, 0, 0));
     }
   }
-  __device__ __forceinline__ void store(char* lds, int tid) const {
+  __device__ __forceinline__ void store(char* lds, uint32_t tid) const {
 #pragma unroll
-    for (int q = 0; q < kN; ++q) {
-      const int i = tid + q * kThreads, r = i / kPer;
-      *reinterpret_cast<u4*>(lds + at(r, (i - r * kPer) * 16)) = v[q];
-    }
+    for (int q = 0; q < kN; ++q)
+      *reinterpret_cast<u4*>(lds + at(tid / kPer + q * (NT / kPer), tid % kPer * 16)) = v[q];
   }
 
-  // Row-major operands, k-values 32 kb + 8 g .. of row 16 i + l15.
-  static __device__ __forceinline__ uint32_t row_base(int l15, int g) { return at(l15, 8 * g * sizeof(T)); }
+  // Row-major operands, k-values 32 kb + 8 g .. of row spread(i, l15).
+  static __device__ __forceinline__ uint32_t row_base(int l15, int g) { return at(spread(0, l15), 8 * g * sizeof(T)); }
   static __device__ __forceinline__ Frag<IO> row(const char* lds, uint32_t base, int i, int kb) {
-    const char* p = lds + 16 * i * kRow;
-    const uint32_t a = base ^ (32 * kb * sizeof(T));
+    const char* p = lds + 32 * (i >> 1) * kRow;
+    const uint32_t a = (base ^ (4 * (i & 1) * kRow)) ^ (32 * kb * sizeof(T));
     if constexpr (IO == 1) {
       return Frag<1>{__builtin_bit_cast(bf8, *reinterpret_cast<const u4*>(p + a))};
     } else {
@@ -224,9 +243,8 @@ struct Tile {
     if constexpr (IO == 1) {
       typedef short s4 __attribute__((ext_vector_type(4)));
       typedef __attribute__((address_space(3))) s4* lds_s4;
-      const uint32_t x4 = (exchange(4) << 4);  // rows 4 to 7 of the eight
       const u2 lo = __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(p + a)));
-      const u2 hi = __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(p + 4 * kRow + (a ^ x4))));
+      const u2 hi = __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(p + 4 * kRow + a)));
       const u4 v = {lo.x, lo.y, hi.x, hi.y};
       return Frag<1>{__builtin_bit_cast(bf8, v)};
     } else {
@@ -271,272 +289,75 @@ __device__ __forceinline__ int64_t ws_base(const LaArgs& a, const Place& p, int 
   return ((bh * a.nseg + seg) * a.nsl + p.slice) * (KD * kVS);
 }
 
-// STATE: only the sum that a segment adds to the state (segments 0 .. nseg - 2).
-template <int IO, int KD, bool SEQ, bool STATE>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 1 ? 3 : KD == 64 ? 2 : 1))) void la_kernel(
-    const LaArgs a) {
-  using T = typename Io<IO>::T;
-  using TileK = Tile<IO, KD>;
-  using TileV = Tile<IO, kVS>;
-  using TileA = Tile<IO, kC>;
-  constexpr int kTiles = KD / 16, kKb = KD / 32;
-  __shared__ __attribute__((aligned(512))) char lds[(STATE ? 1 : 2) * TileK::kBytes + (STATE ? 1 : 2) * TileV::kBytes];
-  char* const Ks = lds;
-  char* const Vs = lds + TileK::kBytes;
-  char* const As = Vs + TileV::kBytes;  // [t][s]
-  char* const Qs = As + TileA::kBytes;
-  // powers of lam with their factors: of a score at distance 63 - m (0 from 64 on, above the diagonal), of the
-  // state read at token t, of token s on its way into the state of a chunk of n
-  __shared__ float w_score[80], w_out[kC], w_in[kC];
+// What a workgroup reads: the rows of one operand and head, from the first
+// token on in the direction of the sum.
+struct Rows {
+  const char* p;
+  int64_t step;  // bytes from a token to the next one
+};
+template <typename T>
+__device__ __forceinline__ Rows rows_of(const LaOperand& o, const Place& pl, int rep, int width, int64_t first, bool rev) {
+  const int64_t head = static_cast<int64_t>(o.per_group ? pl.h / rep : pl.h) * width;
+  const int64_t step = o.row * static_cast<int64_t>(sizeof(T));
+  return Rows{reinterpret_cast<const char*>(static_cast<const T*>(o.p) + first * o.row + head), rev ? -step : step};
+}
+__device__ __forceinline__ const char* chunk_of(const Rows& r, int c) {
+  return r.p + static_cast<int64_t>(c) * kC * r.step;
+}
 
-  const Place pl = place(a, STATE ? a.nseg - 1 : a.nseg);
-  if (!pl.live) return;
-  const LaRole& R = a.role[pl.role];
-  int kd = R.kd, vd = R.vd;
-  const int v0 = pl.slice * kVS;
-  if (v0 >= vd) return;
-  // kept in scalar registers, not loaded again in the loop
-  float sc_out = R.sc_out, sc_kv = R.sc_kv;
-  void* out_p = R.out;
-  const bool three = R.state_out != nullptr;
-  int es_out = IO == 0 || R.out_f32 ? 4 : 2, off = R.off, rev_i = R.rev, nheads = a.nheads, seqlen = a.seqlen;
-  asm volatile("" : "+s"(sc_out), "+s"(sc_kv), "+s"(out_p), "+s"(es_out), "+s"(off), "+s"(rev_i), "+s"(nheads),
-               "+s"(seqlen), "+s"(kd), "+s"(vd));
-  const bool rev = rev_i != 0;
-  const int tid = threadIdx.x, lane = tid & 63, l15_ = lane & 15, g_ = lane >> 4;
-  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int rep = a.nheads / a.ngroups, grp = pl.h / rep;
-  const int nchunks = (a.seqlen + kC - 1) / kC;
-  const int c0 = pl.seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, nchunks);
-  const float g2 = a.log_decay[pl.h] * kLog2e;
-  const int64_t row0 = static_cast<int64_t>(pl.b) * a.seqlen;
+// The first tokens of documents among a chunk's 64, as bits (each wave asks
+// for itself, a chunk ahead): a token whose id is not its predecessor's.
+struct Ids {
+  int own, prev;
+  __device__ __forceinline__ void load(const int32_t* seq_idx, int64_t first, bool rev, int c, int seqlen, int lane) {
+    // the 65 ids from the chunk's lowest token (forwards: the one before it) on
+    const int pos = c * kC + lane;
+    const int32_t* low = seq_idx + first + (rev ? -static_cast<int64_t>(c * kC + kC - 1) : c * kC - 1);
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<int32_t*>(low), 0, (kC + 1) * 4, 0x00020000);
+    const bool ok = (pos < seqlen) & (pos > 0);
+    const Order order(rev, kC + 1);
+    own = __builtin_amdgcn_raw_buffer_load_b32(rsrc, in_range(4 * order(lane + 1), ok), 0, 0);
+    prev = __builtin_amdgcn_raw_buffer_load_b32(rsrc, in_range(4 * order(lane), ok), 0, 0);
+  }
+  __device__ __forceinline__ uint64_t begins() const { return __ballot(own != prev); }
+};
+// The last document's first token among those that begin in the chunk (0: none does).
+__device__ __forceinline__ int last_of(uint64_t begins) { return begins ? 63 - __builtin_clzll(begins) : 0; }
 
-  const int64_t first = row0 + (rev ? a.seqlen - 1 : 0);
-  const int64_t es = rev ? -static_cast<int64_t>(sizeof(T)) : static_cast<int64_t>(sizeof(T));
-  const int64_t qs = R.q.row * es, ks = R.k.row * es, vs = R.v.row * es;  // bytes from a token to the next one
-  const T* qp = static_cast<const T*>(R.q.p) + first * R.q.row + static_cast<int64_t>(R.q.per_group ? grp : pl.h) * kd;
-  const T* kp = static_cast<const T*>(R.k.p) + first * R.k.row + static_cast<int64_t>(R.k.per_group ? grp : pl.h) * kd;
-  const T* vp = static_cast<const T*>(R.v.p) + first * R.v.row + static_cast<int64_t>(R.v.per_group ? grp : pl.h) * vd + v0;
+// S^T of one wave: column v0 + spread(wave, l15), k-elements spread(i, 4 g) + r.
+template <int KD>
+struct State {
+  static constexpr int kTiles = KD / 16;
+  f4 t[kTiles];
 
-  // the state of this lane: column v0 + spread(wv, l15), k-elements spread(i, 4 g) + r
-  const int col = v0 + spread(wv, l15_);
-  f4 S[kTiles];
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-  for (int i = 0; i < kTiles; ++i) S[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-  if (!STATE) {
-    if (a.nseg > 1) {
-      // also segment 0, which has the join's copy of state_in: by now the last
-      // segment may have written state_out in its place
-      const float* w = a.ws + ws_base<KD>(a, pl, pl.seg);
+    for (int i = 0; i < kTiles; ++i) t[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  // One head's state [vd][kd] ([kd][vd] where `transposed`), zero beyond kd.
+  __device__ __forceinline__ void load(const float* st, bool transposed, int col, int vd, int kd, int g) {
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i) S[i] = *reinterpret_cast<const f4*>(w + (i * kThreads + tid) * 4);
-    } else if (R.state_in && col < vd) {
-      const float* st = R.state_in + (static_cast<int64_t>(pl.b) * a.nheads + pl.h) * vd * kd;
+    for (int i = 0; i < kTiles; ++i) {
+      const int e = spread(i, 4 * g);
+      if (e >= kd) continue;
+      if (transposed) {
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i) {
-        const int e = spread(i, 4 * g_);
-        if (e >= kd) continue;
-        if (R.state_t) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) S[i][r] = st[static_cast<int64_t>(e + r) * vd + col];
-        } else {
-          S[i] = *reinterpret_cast<const f4*>(st + static_cast<int64_t>(col) * kd + e);
-        }
+        for (int r = 0; r < 4; ++r) t[i][r] = st[static_cast<int64_t>(e + r) * vd + col];
+      } else {
+        t[i] = *reinterpret_cast<const f4*>(st + static_cast<int64_t>(col) * kd + e);
       }
-    }
-    // the two 16x16 tiles above the diagonal that the products read
-    for (int i = tid; i < 512; i += kThreads) {
-      const int t = i >> 8, r = (i >> 4) & 15, c = i & 15;
-      Io<IO>::store(reinterpret_cast<T*>(As + TileA::at(32 * t + r, (32 * t + 16 + c) * sizeof(T))), 0.0f);
     }
   }
-
-  if (!STATE && tid < 80) w_score[tid] = tid < kC ? power(g2, 63 - tid) * (sc_out * sc_kv) : 0.0f;
-  if (!STATE && tid < kC) w_out[tid] = power(g2, tid + off) * sc_out;
-  const float keep_full = power(g2, kC);
-
-  TileK kt, qt;
-  TileV vt;
-  int id_own = 0, id_prev = 0;
-  bool seen = false;  // a document began in this segment
-  auto fetch = [&](int c) {
-    const int rows = min(kC, seqlen - c * kC);
-    auto from = [&](const T* p, int64_t step) {
-      return reinterpret_cast<const T*>(reinterpret_cast<const char*>(p) + static_cast<int64_t>(c) * kC * step);
-    };
-    kt.load(from(kp, ks), ks, rows, kd, tid);
-    vt.load(from(vp, vs), vs, rows, vd - v0, tid);
-    if (!STATE) qt.load(from(qp, qs), qs, rows, kd, tid);
-    if (SEQ) {
-      const int pos = c * kC + lane;
-      id_own = id_prev = 0;
-      if (pos < seqlen && pos > 0) {
-        id_own = a.seq_idx[first + (rev ? -pos : pos)];
-        id_prev = a.seq_idx[first + (rev ? 1 - pos : pos - 1)];
-      }
-    }
-  };
-  fetch(c0);
-
-  const uint32_t row_b = TileK::row_base(l15_, g_), col_b = TileK::col_base(l15_, g_);
-  const uint32_t a_b = TileA::row_base(l15_, g_), v_b = TileV::col_base(l15_, g_);
-  for (int c = c0; c < c1; ++c) {
-    // Renewed in each chunk: the addresses that follow from these would
-    // otherwise all be kept in registers over the whole loop.
-    uint32_t at_row = row_b, at_col = col_b, at_a = a_b, at_v = v_b;
-    int l15 = l15_, g = g_;
-    asm volatile("" : "+v"(at_row), "+v"(at_col), "+v"(at_a), "+v"(at_v), "+v"(l15), "+v"(g));
-    const int n = min(kC, seqlen - c * kC);
-    kt.store(Ks, tid);
-    vt.store(Vs, tid);
-    if (!STATE) qt.store(Qs, tid);
-    if ((c == c0 || n < kC) && tid < kC) w_in[tid] = tid < n ? power(g2, n - off - tid) * sc_kv : 0.0f;
-    // bit s: a document begins at token s of the chunk
-    const uint64_t begins = SEQ ? __ballot(id_own != id_prev) : 0;
-    const int last = begins ? 63 - __builtin_clzll(begins) : 0;  // the last document's first token
-    seen |= begins != 0;
-    __syncthreads();
-    if (c + 1 < c1) fetch(c + 1);
-
-    if (!STATE) {
-      // A^T: rows s, columns t; wave j has the 16 tokens t from 16 j on, and each lane 4 rows s of one column t
-      const int j = wv, t = 16 * j + l15;
-      int from = 0;
-      if (SEQ) {
-        const uint64_t m = begins & (~0ull >> (63 - t));
-        from = m ? 63 - __builtin_clzll(m) : 0;
-      }
-      const char* q_at = Qs + 16 * j * TileK::kRow;
-      char* a_at = As + 16 * j * TileA::kRow;
-      const uint32_t to = TileA::at(l15, 4 * g * sizeof(T));
-      Frag<IO> qf[kKb], kf[kKb];
-#pragma unroll
-      for (int kb = 0; kb < kKb; ++kb) {
-        kf[kb] = TileK::row(Ks, at_row, 0, kb);
-        qf[kb] = TileK::row(q_at, at_row, 0, kb);
-      }
-#pragma unroll 1
-      for (int i = 0; i <= j; ++i) {
-        f4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int kb = 0; kb < kKb; ++kb) acc = mma(kf[kb], qf[kb], acc);
-        const int s = 16 * i + 4 * g;
-        const float* w = w_score + 63 - t + s;
-        const f4 wt = {w[0], w[1], w[2], w[3]};
-        if (i < j) {
-#pragma unroll
-          for (int kb = 0; kb < kKb; ++kb) kf[kb] = TileK::row(Ks + 16 * (i + 1) * TileK::kRow, at_row, 0, kb);
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r)  // chosen, not multiplied, so that masked pairs drop infinities and NaN
-          acc[r] = s + r <= t && s + r >= from ? acc[r] * wt[r] : 0.0f;
-        char* dst = a_at + (to ^ (16 * i * sizeof(T)));  // row t, from column s
-        if (IO == 1) {
-          typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
-          const bf4 v = {static_cast<__bf16>(acc[0]), static_cast<__bf16>(acc[1]), static_cast<__bf16>(acc[2]),
-                         static_cast<__bf16>(acc[3])};
-          *reinterpret_cast<u2*>(dst) = __builtin_bit_cast(u2, v);
-        } else {
-          *reinterpret_cast<f4*>(dst) = acc;
-        }
-      }
-      __syncthreads();
-    }
-
-    Frag<IO> vf[2];
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) vf[kb] = TileV::col(Vs, at_v, wv, kb);
-
-    if (!STATE) {
-      f4 y[4];
-      // the state's part, lam^(t + off) S q_t; `from[j]`: where token t's document begins in the chunk
-      int from[4];
-      auto carried = [&](uint32_t at) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int kb = 0; kb < kKb; ++kb) {
-          Frag<IO> qf[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) qf[j] = TileK::row(Qs, at, j, kb);
-          const Frag<IO> sf = state_frag<IO>(S[2 * kb], S[2 * kb + 1], g);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) y[j] = mma(sf, qf[j], y[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int t = 16 * j + l15;
-          from[j] = 0;
-          bool open = true;  // no document begins between the state and token t
-          if (SEQ) {
-            const uint64_t m = begins & (~0ull >> (63 - t));
-            from[j] = m ? 63 - __builtin_clzll(m) : 0;
-            open = m == 0;
-          }
-          const float w = w_out[t];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) y[j][r] = open ? y[j][r] * w : 0.0f;
-        }
-      };
-      carried(at_row);
-      float bad = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        y[j] = mma(vf[0], TileA::row(As, at_a, j, 0), y[j]);
-        if (j >= 2) y[j] = mma(vf[1], TileA::row(As, at_a, j, 1), y[j]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) bad = fmaf(y[j][r], 0.0f, bad);
-      }
-      // An infinity or NaN in v also reaches the tokens that it is masked for,
-      // as 0 * inf. Where any sum is not finite the sums are taken again, over
-      // the unmasked tokens alone.
-      if (__any(bad != 0.0f)) {
-        uint32_t again = at_row;
-        asm volatile("" : "+v"(again));  // read again, not kept from above
-        carried(again);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int t = 16 * j + l15;
-#pragma unroll 1
-          for (int s = 0; s < kC; ++s) {
-            if (s > t || s < from[j]) continue;
-            const float p = Io<IO>::load(reinterpret_cast<const T*>(As + TileA::at(t, s * sizeof(T))));
-            const T* v = reinterpret_cast<const T*>(Vs + TileV::at(s, spread(wv, 4 * g) * sizeof(T)));
-#pragma unroll
-            for (int r = 0; r < 4; ++r) y[j][r] = fmaf(p, Io<IO>::load(v + r), y[j][r]);
-          }
-        }
-      }
-      // each lane holds 4 consecutive columns of one token; rows from n on and
-      // columns from vd on are out of the buffer's range and dropped
-      const int oc = spread(wv, 4 * g);
-      const uint32_t row_out = static_cast<uint32_t>(nheads) * vd * es_out;
-      const int64_t low = first + (rev ? -static_cast<int64_t>(c * kC + n - 1) : c * kC);
-      char* const out = static_cast<char*>(out_p) + ((low * nheads + pl.h) * vd + v0) * es_out;
-      const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(out, 0, row_out * (n - 1) + (vd - v0) * es_out, 0x00020000);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int t = 16 * j + l15;
-        const uint32_t o = t < n && oc < vd - v0
-                               ? static_cast<uint32_t>(rev ? n - 1 - t : t) * row_out + static_cast<uint32_t>(oc) * es_out
-                               : 0xFFFFFFF0u;
-        if (IO == 0 || es_out == 4) {
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, y[j]), rsrc, o, 0, 0);
-        } else {
-          typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
-          const bf4 v = {static_cast<__bf16>(y[j][0]), static_cast<__bf16>(y[j][1]), static_cast<__bf16>(y[j][2]),
-                         static_cast<__bf16>(y[j][3])};
-          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u2, v), rsrc, o, 0, 0);
-        }
-      }
-    }
-
-    // S^T = lam^n S^T + K^T (w V) over the tokens of the last document
-    const float keep = n == kC ? keep_full : power(g2, n);
+  // S^T = lam^n S^T + K^T (w V) over the tokens of the last document; w_in
+  // holds the tokens' weights, keep is lam^n.
+  template <int IO, bool SEQ, typename TileK>
+  __device__ __forceinline__ void add(const char* Ks, uint32_t at_col, const Frag<IO> (&vf)[2], const float* w_in,
+                                      float keep, uint64_t begins, int g, bool three) {
+    const int last = SEQ ? last_of(begins) : 0;
 #pragma unroll
     for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) S[i][r] = begins ? 0.0f : S[i][r] * keep;
+      for (int r = 0; r < 4; ++r) t[i][r] = SEQ && begins ? 0.0f : t[i][r] * keep;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
       float x[8];
@@ -547,8 +368,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 
         x[j] = frag_get(vf[kb], j) * w[j >> 2][j & 3];
         if (SEQ) x[j] = 32 * kb + 8 * g + j >= last ? x[j] : 0.0f;
       }
-      Weighted<IO> wvf;
-      wvf.set(x, three);
+      Weighted<IO> wv;
+      wv.set(x, three);
       // four tiles at a time: their operands first, then one product with each part in turn
 #pragma unroll
       for (int i0 = 0; i0 < kTiles; i0 += 4) {
@@ -556,40 +377,412 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           kf[i] = TileK::col(Ks, at_col, i0 + i, kb);
+          // keys of other documents may hold infinities or NaN, which a weight of 0 would not remove
           if (SEQ) kf[i] = frag_from(kf[i], last - (32 * kb + 8 * g));
         }
 #pragma unroll
         for (int p = Weighted<IO>::kParts - 1; p >= 0; --p) {
           if (p == 2 && !three) continue;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) S[i0 + i] = mma(kf[i], wvf.part[p], S[i0 + i]);
+          for (int i = 0; i < 4; ++i) t[i0 + i] = mma(kf[i], wv.part[p], t[i0 + i]);
         }
       }
     }
+  }
+};
+
+template <int IO, int KD>
+struct Plan {
+  using T = typename Io<IO>::T;
+  static constexpr int kThreadsY = 2 * kThreads;
+  using TileK = Tile<IO, KD, kThreadsY>;
+  using TileV = Tile<IO, kVS, kThreadsY>;
+  using TileS = Tile<IO, KD, kThreadsY>;  // [column of v][k-element]
+  // the state once in LDS, with a second barrier, where twice would not fit
+  static constexpr int kSBuf = 2 * (TileK::kBytes + TileV::kBytes + TileS::kBytes) + 1024 <= 160 * 1024 ? 2 : 1;
+};
+
+template <int IO, int KD, bool SEQ>
+__global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO == 1 ? 4 : 2))) void la_kernel(
+    const LaArgs a) {
+  using P = Plan<IO, KD>;
+  using T = typename Io<IO>::T;
+  using TileK = typename P::TileK;
+  using TileV = typename P::TileV;
+  using TileS = typename P::TileS;
+  constexpr int kKb = KD / 32, kSBuf = P::kSBuf;
+  constexpr uint32_t kBufK = 0, kBufV = 2 * TileK::kBytes, kBufS = kBufV + 2 * TileV::kBytes;
+  __shared__ __attribute__((aligned(512))) char lds[kBufS + kSBuf * TileS::kBytes];
+  // powers of lam with their factors: of a score at distance 63 - m (0 from 64
+  // on, above the diagonal), and of token s on its way into the state, for a
+  // whole chunk and for the last one
+  __shared__ float w_score[96], w_in[2][kC];
+
+  const Place pl = place(a, a.nseg);
+  if (!pl.live) return;
+  const LaRole& R = a.role[pl.role];
+  int kd = R.kd, vd = R.vd;
+  const int v0 = pl.slice * kVS;
+  if (v0 >= vd) return;
+  // kept in scalar registers, not loaded again in the loop
+  float sc_out = R.sc_out, sc_kv = R.sc_kv;
+  void* out_p = R.out;
+  int es_out = IO == 0 || R.out_f32 ? 4 : 2, off = R.off, rev_i = R.rev, nheads = a.nheads, seqlen = a.seqlen;
+  int three_i = __builtin_amdgcn_readfirstlane(R.state_out != nullptr);
+  asm volatile("" : "+s"(sc_out), "+s"(sc_kv), "+s"(out_p), "+s"(es_out), "+s"(off), "+s"(rev_i), "+s"(nheads),
+               "+s"(seqlen), "+s"(kd), "+s"(vd), "+s"(three_i));
+  const bool rev = rev_i != 0, three = three_i != 0;
+  const int tid = threadIdx.x, lane = tid & 63, l15 = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wv = wave & 3;
+  const bool makes_y = wave < 4;
+  const int rep = a.nheads / a.ngroups;
+  const int nchunks = (seqlen + kC - 1) / kC;
+  const int c0 = pl.seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, nchunks);
+  const float g2 = a.log_decay[pl.h] * kLog2e;
+  const int64_t first = static_cast<int64_t>(pl.b) * seqlen + (rev ? seqlen - 1 : 0);
+  const Rows qr = rows_of<T>(R.q, pl, rep, kd, first, rev), kr = rows_of<T>(R.k, pl, rep, kd, first, rev);
+  Rows vr = rows_of<T>(R.v, pl, rep, vd, first, rev);
+  vr.p += v0 * sizeof(T);
+
+  const float keep_full = power(g2, kC);
+
+  TileK kt[2];
+  TileV vt[2];
+  Ids ids[2];
+  auto fetch = [&](int c, TileK& k, TileV& v) {
+    const int n = c < c1 ? min(kC, seqlen - c * kC) : 0;
+    k.load(chunk_of(kr, c), kr.step, n, kd, tid);
+    v.load(chunk_of(vr, c), vr.step, n, vd - v0, tid);
+  };
+  auto start = [&]() {
+    fetch(c0, kt[0], vt[0]);
+    fetch(c0 + 1, kt[1], vt[1]);
+    if (SEQ) ids[0].load(a.seq_idx, first, rev, c0, seqlen, lane);
+  };
+  // A chunk's beginning, for either task: the tiles two chunks on start their
+  // way, and the wave learns where documents begin.
+  auto begin = [&](int c, auto parity) {
+    constexpr int par = decltype(parity)::value;
+    fetch(c + 2, kt[par], vt[par]);
+    const uint64_t begins = SEQ ? ids[par].begins() : 0;
+    if (SEQ) ids[par ^ 1].load(a.seq_idx, first, rev, c + 1, seqlen, lane);
+    return begins;
+  };
+  auto put_tiles = [&](auto parity) {
+    constexpr int par = decltype(parity)::value;
+    kt[par].store(lds + kBufK + par * TileK::kBytes, tid);
+    vt[par].store(lds + kBufV + par * TileV::kBytes, tid);
+  };
+  // The two tasks run loops of their own, so that neither holds the other's
+  // registers; they meet at the same number of barriers.
+  auto all_chunks = [&](auto&& chunk) {
+    using Even = std::integral_constant<int, 0>;
+    using Odd = std::integral_constant<int, 1>;
+    put_tiles(Even{});
     __syncthreads();
+    for (int c = c0; c < c1; c += 2) {  // the second of the last two may be empty
+      chunk(c, Even{});
+      put_tiles(Odd{});
+      __syncthreads();
+      chunk(c + 1, Odd{});
+      put_tiles(Even{});
+      __syncthreads();
+    }
+  };
+
+  if (!makes_y) {
+    const int col = v0 + spread(wv, l15);
+    State<KD> S;
+    // writes this wave's columns of S to the chunk's tile, in the io type
+    // (rounded to bfloat16: the choice that makes y's products plain ones)
+    auto put_state = [&](char* to) {
+#pragma unroll
+      for (int i = 0; i < State<KD>::kTiles; ++i) {
+        char* dst = to + TileS::at(spread(wv, l15), spread(i, 4 * g) * sizeof(T));
+        if constexpr (IO == 1) {
+          typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
+          const bf4 v = {static_cast<__bf16>(S.t[i][0]), static_cast<__bf16>(S.t[i][1]),
+                         static_cast<__bf16>(S.t[i][2]), static_cast<__bf16>(S.t[i][3])};
+          *reinterpret_cast<u2*>(dst) = __builtin_bit_cast(u2, v);
+        } else {
+          *reinterpret_cast<f4*>(dst) = S.t[i];
+        }
+      }
+    };
+    start();
+    S.zero();
+    if (a.nseg > 1) {
+      // also segment 0, which has the join's copy of state_in: by now the last
+      // segment may have written state_out in its place
+      const float* w = a.ws + ws_base<KD>(a, pl, pl.seg);
+#pragma unroll
+      for (int i = 0; i < State<KD>::kTiles; ++i)
+        S.t[i] = *reinterpret_cast<const f4*>(w + (i * kThreads + (tid & (kThreads - 1))) * 4);
+    } else if (R.state_in && col < vd) {
+      S.load(R.state_in + (static_cast<int64_t>(pl.b) * nheads + pl.h) * vd * kd, R.state_t, col, vd, kd, g);
+    }
+    put_state(lds + kBufS);
+    if (wv < 2) {
+      const int n = wv == 0 ? kC : seqlen - (nchunks - 1) * kC;
+      w_in[wv][lane] = lane < n ? power(g2, n - off - lane) * sc_kv : 0.0f;
+    }
+    const uint32_t col_k = TileK::col_base(l15, g);
+    const uint32_t col_v = TileV::col_base(l15, g) ^ ((wv >> 1) * 32 + (wv & 1) * 4) * sizeof(T);
+    all_chunks([&](int c, auto parity) {
+      constexpr int par = decltype(parity)::value;
+      const int n = min(kC, seqlen - c * kC);
+      const uint64_t begins = begin(c, parity);
+      uint32_t at_col = col_k, at_v = col_v;  // renewed: what follows from them is not kept over the loop
+      int gg = g;
+      asm volatile("" : "+v"(at_col), "+v"(at_v), "+v"(gg));
+      if (c < c1) {
+        Frag<IO> vf[2];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) vf[kb] = TileV::col(lds + kBufV + par * TileV::kBytes, at_v, 0, kb);
+        const float keep = n == kC ? keep_full : power(g2, n);
+        S.template add<IO, SEQ, TileK>(lds + kBufK + par * TileK::kBytes, at_col, vf, w_in[n < kC], keep, begins, gg, three);
+      }
+      if (kSBuf == 1) __syncthreads();  // the chunk's starting state has been read
+      put_state(lds + kBufS + (kSBuf == 2 ? par ^ 1 : 0) * TileS::kBytes);
+    });
+    if (c1 == nchunks && R.state_out && col < vd) {
+      float* st = R.state_out + (static_cast<int64_t>(pl.b) * nheads + pl.h) * vd * kd + static_cast<int64_t>(col) * kd;
+#pragma unroll
+      for (int i = 0; i < State<KD>::kTiles; ++i) {
+        const int e = spread(i, 4 * g);
+        if (e < kd) *reinterpret_cast<f4*>(st + e) = S.t[i];
+      }
+    }
+    return;
   }
 
-  if (STATE) {
-    float* w = a.ws + ws_base<KD>(a, pl, pl.seg + 1);
+  // the wave's 16 tokens of q as operands; 0 beyond the sequence and beyond kd
+  Frag<IO> q[2][kKb];
+  auto fetch_q = [&](int c, Frag<IO> (&f)[kKb]) {
+    const int n = c < c1 ? min(kC, seqlen - c * kC) : 0;
+    const uint32_t stride = static_cast<uint32_t>(rev ? -qr.step : qr.step);
+    const Order order(rev, n);
+    const char* low = chunk_of(qr, c) + qr.step * order.base;
+    const uint32_t bytes = n > 0 ? stride * static_cast<uint32_t>(n - 1) + kd * static_cast<uint32_t>(sizeof(T)) : 0;
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(low), 0, bytes, 0x00020000);
+    const int t = 16 * wv + l15;
+    const uint32_t at = order(t) * stride;
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) *reinterpret_cast<f4*>(w + (i * kThreads + tid) * 4) = S[i];
-    if (SEQ && tid == 0) {
-      // every head and slice of the row writes the same value
-      a.flags[(pl.role * a.batch + pl.b) * a.nseg + pl.seg] = seen ? 1 : 0;
+    for (int kb = 0; kb < kKb; ++kb) {
+      const int e = 32 * kb + 8 * g;
+      const uint32_t o = in_range(at + e * sizeof(T), (t < n) & (e < kd));
+      const u4 x = __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, o, 0, 0));
+      if constexpr (IO == 1) {
+        f[kb] = Frag<1>{__builtin_bit_cast(bf8, x)};
+      } else {
+        const u4 y = __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, o + 16, 0, 0));
+        f[kb] = Frag<0>{__builtin_bit_cast(f4, x), __builtin_bit_cast(f4, y)};
+      }
     }
-  } else if (c1 == nchunks && R.state_out && col < vd) {
-    float* st = R.state_out + (static_cast<int64_t>(pl.b) * a.nheads + pl.h) * vd * kd + static_cast<int64_t>(col) * kd;
+  };
+  start();
+  fetch_q(c0, q[0]);
+  fetch_q(c0 + 1, q[1]);
+  if (tid < 96) w_score[tid] = tid < kC ? power(g2, 63 - tid) * (sc_out * sc_kv) : 0.0f;
+  const float w_out = power(g2, 16 * wv + l15 + off) * sc_out;  // of the state read at this lane's token
+  const uint32_t row_b = TileK::row_base(l15, g), col_v = TileV::col_base(l15, g);
+  all_chunks([&](int c, auto parity) {
+    constexpr int par = decltype(parity)::value;
+    const int n = c < c1 ? min(kC, seqlen - c * kC) : 0;
+    const char* const Ks = lds + kBufK + par * TileK::kBytes;
+    const char* const Vs = lds + kBufV + par * TileV::kBytes;
+    const char* const Ss = lds + kBufS + (kSBuf == 2 ? par : 0) * TileS::kBytes;
+    const uint64_t begins = begin(c, parity);
+    uint32_t at_row = row_b, at_v = col_v;  // renewed: what follows from them is not kept over the loop
+    int t = 16 * wv + l15, gg = g;
+    asm volatile("" : "+v"(at_row), "+v"(at_v), "+v"(t), "+v"(gg));
+    int from = 0;      // where token t's document begins in the chunk
+    bool open = true;  // no document begins between the state and token t
+    if (SEQ) {
+      const uint64_t m = begins & (~0ull >> (63 - t));
+      from = last_of(m);
+      open = m == 0;
+    }
+    f4 y[4];  // columns t, rows spread(i, 4 g) + r of the 64 columns of v
+    if (c < c1) {
+      // the scores: columns t, rows s; tiles 0 and 1 have s < 32, the other two are needed by the upper 32 tokens
+      f4 sc[4];
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) {
-      const int e = spread(i, 4 * g_);
-      if (e < kd) *reinterpret_cast<f4*>(st + e) = S[i];
+      for (int h = 0; h < 2; ++h) {
+        sc[2 * h] = sc[2 * h + 1] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (h == 1 && wv < 2) break;
+#pragma unroll
+        for (int kb = 0; kb < kKb; ++kb)
+#pragma unroll
+          for (int i = 2 * h; i < 2 * h + 2; ++i) sc[i] = mma(TileK::row(Ks, at_row, i, kb), q[par][kb], sc[i]);
+#pragma unroll
+        for (int i = 2 * h; i < 2 * h + 2; ++i) {
+          const int s = spread(i, 4 * gg);
+          const float* w = w_score + 63 - t + s;
+          const f4 wt = {w[0], w[1], w[2], w[3]};
+#pragma unroll
+          for (int r = 0; r < 4; ++r)  // chosen, not multiplied, so that masked pairs drop infinities and NaN
+            sc[i][r] = ((s + r <= t) & (s + r >= from)) ? sc[i][r] * wt[r] : 0.0f;
+        }
+      }
+      auto carried = [&](uint32_t at) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int kb = 0; kb < kKb; ++kb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[i] = mma(TileS::row(Ss, at, i, kb), q[par][kb], y[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) y[i][r] = open ? y[i][r] * w_out : 0.0f;
+      };
+      carried(at_row);
+      // the scores are rounded to the io type here, once
+      const Frag<IO> s0 = state_frag<IO>(sc[0], sc[1], gg), s1 = state_frag<IO>(sc[2], sc[3], gg);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = mma(TileV::col(Vs, at_v, i, 0), s0, y[i]);
+      if (wv >= 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = mma(TileV::col(Vs, at_v, i, 1), s1, y[i]);
+      }
+      float bad = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) bad = fmaf(y[i][r], 0.0f, bad);
+      // An infinity or NaN in v also reaches the tokens that it is masked for,
+      // as 0 * inf. Where any sum is not finite the sums are taken again, over
+      // the unmasked tokens alone.
+      if (__any(bad != 0.0f)) {
+        uint32_t again = at_row;
+        asm volatile("" : "+v"(again));  // read again, not kept from above
+        carried(again);
+#pragma unroll 1
+        for (int gs = 0; gs < 4; ++gs) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int s = 32 * (k >> 3) + 8 * gs + (k & 7);
+            const float p = __shfl(k < 8 ? frag_get(s0, k & 7) : frag_get(s1, k & 7), 16 * gs + l15, 64);
+            if (s > t || s < from) continue;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const T* v = reinterpret_cast<const T*>(Vs + TileV::at(s, spread(i, 4 * gg) * sizeof(T)));
+#pragma unroll
+              for (int r = 0; r < 4; ++r) y[i][r] = fmaf(p, Io<IO>::load(v + r), y[i][r]);
+            }
+          }
+        }
+      }
     }
+    if (kSBuf == 1) __syncthreads();  // the chunk's starting state has been read
+    fetch_q(c + 2, q[par]);
+    // Two tiles are 8 neighbouring columns of a token, the upper four first
+    // where g is odd. Rows from n on and columns from vd on are out of the
+    // buffer's range and dropped.
+    const uint32_t row_out = static_cast<uint32_t>(nheads) * vd * es_out;
+    const Order order(rev, n);
+    const int64_t low = first + (rev ? -1 : 1) * static_cast<int64_t>(c * kC + order.base);
+    char* const out = static_cast<char*>(out_p) + ((low * nheads + pl.h) * vd + v0) * es_out;
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(out, 0, n > 0 ? row_out * (n - 1) + (vd - v0) * es_out : 0, 0x00020000);
+    const uint32_t o_row = order(t) * row_out;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int oc = 32 * h + 8 * gg;
+      const uint32_t o = in_range(o_row + oc * es_out, (t < n) & (oc < vd - v0));
+      if (IO == 0 || es_out == 4) {
+        const bool up = gg & 1;
+        const f4 lo = up ? y[2 * h + 1] : y[2 * h], hi = up ? y[2 * h] : y[2 * h + 1];
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, lo), rsrc, o, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, hi), rsrc, o + 16, 0, 0);
+      } else {
+        const Frag<1> v = state_frag<1>(y[2 * h], y[2 * h + 1], gg);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, v.v), rsrc, o, 0, 0);
+      }
+    }
+  });
+}
+
+// What each segment but the last adds to the state: the state's task alone,
+// four waves to a workgroup.
+template <int IO, int KD, bool SEQ>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 1 ? 3 : 1))) void la_sum_kernel(
+    const LaArgs a) {
+  using T = typename Io<IO>::T;
+  using TileK = Tile<IO, KD, kThreads>;
+  using TileV = Tile<IO, kVS, kThreads>;
+  constexpr uint32_t kBufV = 2 * TileK::kBytes;
+  __shared__ __attribute__((aligned(512))) char lds[kBufV + 2 * TileV::kBytes];
+  __shared__ float w_in[kC];
+
+  const Place pl = place(a, a.nseg - 1);
+  if (!pl.live) return;
+  const LaRole& R = a.role[pl.role];
+  const int kd = R.kd, vd = R.vd, v0 = pl.slice * kVS, seqlen = a.seqlen;
+  if (v0 >= vd) return;
+  const bool rev = R.rev;
+  const int tid = threadIdx.x, lane = tid & 63, l15 = lane & 15, g = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int rep = a.nheads / a.ngroups;
+  const int c0 = pl.seg * a.seg_chunks, c1 = c0 + a.seg_chunks;  // whole chunks: a later segment follows
+  const float g2 = a.log_decay[pl.h] * kLog2e;
+  const int64_t first = static_cast<int64_t>(pl.b) * seqlen + (rev ? seqlen - 1 : 0);
+  const Rows kr = rows_of<T>(R.k, pl, rep, kd, first, rev);
+  Rows vr = rows_of<T>(R.v, pl, rep, vd, first, rev);
+  vr.p += v0 * sizeof(T);
+  const bool three = __builtin_amdgcn_readfirstlane(R.state_out != nullptr) != 0;
+
+  TileK kt[2];
+  TileV vt[2];
+  Ids ids[2];
+  auto fetch = [&](int c, TileK& k, TileV& v) {
+    const int n = c < c1 ? kC : 0;
+    k.load(chunk_of(kr, c), kr.step, n, kd, tid);
+    v.load(chunk_of(vr, c), vr.step, n, vd - v0, tid);
+  };
+  fetch(c0, kt[0], vt[0]);
+  fetch(c0 + 1, kt[1], vt[1]);
+  if (SEQ) ids[0].load(a.seq_idx, first, rev, c0, seqlen, lane);
+  if (tid < kC) w_in[tid] = power(g2, kC - R.off - tid) * R.sc_kv;
+  const float keep = power(g2, kC);
+  State<KD> S;
+  S.zero();
+  bool seen = false;  // a document began in this segment
+  kt[0].store(lds, tid);
+  vt[0].store(lds + kBufV, tid);
+  __syncthreads();
+  auto chunk = [&](int c, auto parity) {
+    constexpr int par = decltype(parity)::value;
+    const char* const Vs = lds + kBufV + par * TileV::kBytes;
+    fetch(c + 2, kt[par], vt[par]);
+    const uint64_t begins = SEQ && c < c1 ? ids[par].begins() : 0;
+    seen |= begins != 0;
+    if (SEQ) ids[par ^ 1].load(a.seq_idx, first, rev, c + 1, seqlen, lane);
+    if (c < c1) {
+      const uint32_t at_v = TileV::col_base(l15, g) ^ ((wv >> 1) * 32 + (wv & 1) * 4) * sizeof(T);
+      Frag<IO> vf[2];
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) vf[kb] = TileV::col(Vs, at_v, 0, kb);
+      S.template add<IO, SEQ, TileK>(lds + par * TileK::kBytes, TileK::col_base(l15, g), vf, w_in, keep, begins, g, three);
+    }
+    kt[par ^ 1].store(lds + (par ^ 1) * TileK::kBytes, tid);
+    vt[par ^ 1].store(lds + kBufV + (par ^ 1) * TileV::kBytes, tid);
+    __syncthreads();
+  };
+  for (int c = c0; c < c1; c += 2) {  // the second of the last two may be empty
+    chunk(c, std::integral_constant<int, 0>{});
+    chunk(c + 1, std::integral_constant<int, 1>{});
   }
+  float* w = a.ws + ws_base<KD>(a, pl, pl.seg + 1);
+#pragma unroll
+  for (int i = 0; i < State<KD>::kTiles; ++i) *reinterpret_cast<f4*>(w + (i * kThreads + tid) * 4) = S.t[i];
+  // every head and slice of the row writes the same value
+  if (SEQ && tid == 0) a.flags[(pl.role * a.batch + pl.b) * a.nseg + pl.seg] = seen ? 1 : 0;
 }
 
 // The state before each segment: entry 0 is the incoming state, and entry j,
 // which holds the sum of segment j - 1 alone, becomes lam^len entry (j - 1) +
-// entry j. One thread per 4 elements, in the order in which la_kernel keeps them.
+// entry j. One thread per 4 elements, in the order in which State keeps them.
 template <int KD, bool SEQ>
 __global__ __launch_bounds__(kThreads) void la_join_kernel(const LaArgs a) {
   constexpr int kTiles = KD / 16;
@@ -637,7 +830,7 @@ hipError_t launch_typed(const LaCall& c, const LaPlan& p, const LaArgs& a) {
     return dim3(static_cast<unsigned>((units + 7) / 8 * 8 * sub));
   };
   if (p.nseg > 1) {
-    hipLaunchKernelGGL((la_kernel<IO, KD, SEQ, true>), grid(p.nseg - 1), dim3(kThreads), 0, c.stream, a);
+    hipLaunchKernelGGL((la_sum_kernel<IO, KD, SEQ>), grid(p.nseg - 1), dim3(kThreads), 0, c.stream, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const unsigned joins = static_cast<unsigned>(KD / 16) * a.nsl * a.nroles * a.nheads * a.batch;
@@ -645,7 +838,7 @@ hipError_t launch_typed(const LaCall& c, const LaPlan& p, const LaArgs& a) {
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((la_kernel<IO, KD, SEQ, false>), grid(p.nseg), dim3(kThreads), 0, c.stream, a);
+  hipLaunchKernelGGL((la_kernel<IO, KD, SEQ>), grid(p.nseg), dim3(2 * kThreads), 0, c.stream, a);
   return hipGetLastError();
 }
 
