@@ -13,13 +13,15 @@
 // anyway, and nothing of the forward has to be kept.
 //
 // All tensors are read and written once, so both directions are bound by
-// memory traffic. A group is held in registers by 1 to 64 lanes of one wave
-// (the power of two that covers it with 16-byte pieces, up to 4 pieces a
-// lane), or by a whole workgroup of 256 to 1024 threads; the mean is taken
-// first and the squares of what is left of it, in float32. A wave takes
-// several neighbouring groups of a row, and several rows, where groups are
-// small; it keeps its channels from row to row, so that the sums over rows
-// stay in registers and leave as one partial sum per workgroup, which a second
+// memory traffic, and by how much of it is under way. A group of up to 512
+// bytes' worth of 16-byte pieces, one a lane, is held by 1 to 64 lanes of one
+// wave, which takes several neighbouring groups and several rows at a time; a
+// larger one by a workgroup of up to 16 waves, one or a few pieces a lane,
+// whose waves' sums meet in LDS (a wave that held all of 1536 channels would
+// need 300 registers in the backward and leave its SIMD with one wave). The
+// mean is taken first and the squares of what is left of it, in float32.
+// Lanes keep their channels from row to row, so that the sums over rows stay
+// in registers and leave as one partial sum per workgroup, which a second
 // kernel adds in a fixed order.
 #include "gnorm_internal.h"
 #include "mfma_frag.h"
@@ -30,7 +32,7 @@ namespace mscan {
 namespace {
 
 constexpr int kWaves = 4;            // waves per workgroup where a wave holds whole groups
-constexpr int kGateNone = 0, kGateAfter = 1, kGateFirst = 2;
+constexpr int kGateNone = 0, kGateAfter = 1, kGateFirst = 2, kGateAny = 3;
 constexpr int kActNone = 0, kActSilu = 1;  // 2: sigmoid
 
 struct GnArgs {
@@ -80,9 +82,9 @@ __device__ __forceinline__ void put(typename Io<IO>::T* p, const float (&o)[V]) 
     const bf8 v = {static_cast<__bf16>(o[0]), static_cast<__bf16>(o[1]), static_cast<__bf16>(o[2]),
                    static_cast<__bf16>(o[3]), static_cast<__bf16>(o[4]), static_cast<__bf16>(o[5]),
                    static_cast<__bf16>(o[6]), static_cast<__bf16>(o[7])};
-    *reinterpret_cast<u4*>(p) = __builtin_bit_cast(u4, v);
+    __builtin_nontemporal_store(__builtin_bit_cast(u4, v), reinterpret_cast<u4*>(p));
   } else {
-    *reinterpret_cast<f4*>(p) = f4{o[0], o[1], o[2], o[3]};
+    __builtin_nontemporal_store(f4{o[0], o[1], o[2], o[3]}, reinterpret_cast<f4*>(p));
   }
 }
 template <int IO, int V>
@@ -90,6 +92,25 @@ __device__ __forceinline__ Vec<IO, V> fetch(const void* base, int64_t at, bool o
   Vec<IO, V> r{};
   if (ok) r = *reinterpret_cast<const Vec<IO, V>*>(static_cast<const typename Io<IO>::T*>(base) + at);
   return r;
+}
+
+// V parameters of a lane's channels, `otherwise` where there are none.
+template <int V>
+__device__ __forceinline__ void fetch_params(const float* p, int at, bool ok, float otherwise, float (&o)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) o[i] = otherwise;
+  if (!p || !ok) return;
+  if constexpr (V == 1) {
+    o[0] = p[at];
+  } else {
+    typedef float f4a __attribute__((ext_vector_type(4), aligned(4)));
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const f4a v = *reinterpret_cast<const f4a*>(p + at + i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[i + j] = v[j];
+    }
+  }
 }
 
 template <int CTRL>
@@ -119,16 +140,23 @@ __device__ __forceinline__ float lanes_sum(float v, int ln) {
   return v;
 }
 
-// The same over a whole workgroup; `red` holds one float per wave.
-__device__ __forceinline__ float wide_sum(float v, float* red) {
-  v = lanes_sum(v, 64);
+// The same over a whole workgroup, N sums at once. Each call takes the other
+// half of `red` than the call before it, so that one barrier does: who writes
+// a half again has passed the barrier behind its last reading.
+template <int N>
+__device__ __forceinline__ void wide_sum(float (&v)[N], float (&red)[2][N][16], int half) {
   const int waves = static_cast<int>(blockDim.x) >> 6;
-  __syncthreads();  // the last sum's readers are done
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    v[i] = lanes_sum(v[i], 64);
+    if ((threadIdx.x & 63) == 0) red[half][i][threadIdx.x >> 6] = v[i];
+  }
   __syncthreads();
-  v = red[0];
-  for (int w = 1; w < waves; ++w) v += red[w];
-  return v;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    v[i] = red[half][i][0];
+    for (int w = 1; w < waves; ++w) v[i] += red[half][i][w];
+  }
 }
 
 // sigmoid(z) and 1 - sigmoid(z), the latter without cancellation. The exponent
@@ -142,37 +170,58 @@ __device__ __forceinline__ Sig sigmoid(float z) {
   const float e = exp2_hw(t), s = rcp_hw(1.0f + e);
   return Sig{s, e * s};
 }
+// Chosen by value, not by branch: the kind is the same for a whole launch, and
+// a branch at each element would keep the elements from overlapping.
 __device__ __forceinline__ float act(int kind, float z) {
-  if (kind == kActNone) return z;
   const float s = sigmoid(z).s;
-  return kind == kActSilu ? z * s : s;
+  const float a = kind == kActSilu ? z * s : s;
+  return kind == kActNone ? z : a;
 }
 // activation and its derivative
 __device__ __forceinline__ float act_grad(int kind, float z, float& a) {
-  if (kind == kActNone) {
-    a = z;
-    return 1.0f;
-  }
   const Sig g = sigmoid(z);
-  a = kind == kActSilu ? z * g.s : g.s;
-  return kind == kActSilu ? g.s * fmaf(z, g.c, 1.0f) : g.s * g.c;
+  const float b = kind == kActSilu ? z * g.s : g.s;
+  a = kind == kActNone ? z : b;
+  const float d = g.s * (kind == kActSilu ? fmaf(z, g.c, 1.0f) : g.c);
+  return kind == kActNone ? 1.0f : d;
 }
 
-// V elements a piece, K pieces a lane. WIDE: one group of one row per workgroup.
-template <int IO, int V, int K, bool WIDE, bool BWD>
+// V elements a piece, K pieces a lane, U rows at a time. WIDE: one group of
+// one row per workgroup. GATE: one of the three, or kGateAny where the call says.
+template <int IO, int V, int K, int U, bool WIDE, bool BWD, int GATE>
 __global__ __launch_bounds__(WIDE ? 1024 : 64 * kWaves) void gnorm_kernel(const GnArgs a) {
   using T = typename Io<IO>::T;
-  __shared__ float red[WIDE ? 16 : 1];
+  const int gate_kind = GATE == kGateAny ? a.gate : GATE;
+  static_assert(!WIDE || U == 1, "a workgroup's sums meet row by row");
+  __shared__ float red[2][2][WIDE ? 16 : 1];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int tile = blockIdx.x % a.tiles, blk = blockIdx.x / a.tiles;
   const int in = WIDE ? tid : lane & (a.ln - 1);              // lane within its group
   const int slot = WIDE ? 0 : lane >> a.ln_log;               // which of the wave's groups
   const int sub = WIDE ? 0 : slot / a.gp;                     // which of the wave's rows
-  const int rp = WIDE ? 1 : 64 / (a.ln * a.gp);               // rows of a wave
+  const int rp = WIDE ? 1 : 64 / (a.ln * a.gp);               // rows side by side in a wave
   const int ch0 = (tile * a.gp + (slot - sub * a.gp)) * a.gs;  // the group's first channel
   const int lanes = WIDE ? static_cast<int>(blockDim.x) : a.ln;
   const float inv = 1.0f / static_cast<float>(a.gs);
-  auto sum = [&](float v) { return WIDE ? wide_sum(v, red) : lanes_sum(v, a.ln); };
+  int half = 0;
+  auto sum = [&](float (&v)[2]) {  // over the group, in all of its lanes
+    if constexpr (WIDE) {
+      wide_sum(v, red, half);
+      half ^= 1;
+    } else {
+      v[0] = lanes_sum(v[0], a.ln);
+      v[1] = lanes_sum(v[1], a.ln);
+    }
+  };
+  auto sum1 = [&](float v) {
+    float w[2] = {v, 0.0f};
+    if constexpr (WIDE) {
+      sum(w);
+      return w[0];
+    } else {
+      return lanes_sum(v, a.ln);
+    }
+  };
 
   int ch[K];
   bool in_group[K];
@@ -182,123 +231,137 @@ __global__ __launch_bounds__(WIDE ? 1024 : 64 * kWaves) void gnorm_kernel(const 
     const int e = (p * lanes + in) * V;
     in_group[p] = e < a.gs;
     ch[p] = ch0 + e;
+    fetch_params<V>(a.weight, ch[p], in_group[p], 1.0f, w[p]);
+    fetch_params<V>(a.bias, ch[p], in_group[p], 0.0f, b[p]);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      w[p][i] = in_group[p] && a.weight ? a.weight[ch[p] + i] : 1.0f;
-      b[p][i] = in_group[p] && a.bias ? a.bias[ch[p] + i] : 0.0f;
+    for (int i = 0; i < V; ++i)
       if (BWD) sw[p][i] = sb[p][i] = 0.0f;
-    }
   }
 
-  const int64_t per = WIDE ? 1 : static_cast<int64_t>(kWaves) * rp;  // rows of a workgroup
-  int64_t row0 = blk * per + (WIDE ? 0 : static_cast<int64_t>(wave) * rp);  // uniform in the wave
-  Vec<IO, V> rx[K], rz[K], rd[BWD ? K : 1];
+  const int64_t per = WIDE ? 1 : static_cast<int64_t>(kWaves) * U * rp;  // rows of a workgroup at a time
+  int64_t row0 = blk * per + (WIDE ? 0 : static_cast<int64_t>(wave) * U * rp);  // uniform in the wave
+  Vec<IO, V> rx[U][K], rz[U][K], rd[BWD ? U : 1][K];
   auto load = [&](int64_t r0) {
-    const int64_t row = r0 + sub;
 #pragma unroll
-    for (int p = 0; p < K; ++p) {
-      const bool ok = in_group[p] && row < a.rows;
-      rx[p] = fetch<IO, V>(a.x, row * a.x_row + ch[p], ok);
-      if (a.gate != kGateNone) rz[p] = fetch<IO, V>(a.z, row * a.z_row + ch[p], ok);
-      if (BWD) rd[p] = fetch<IO, V>(a.dy, row * a.dy_row + ch[p], ok);
-    }
-  };
-  if (row0 < a.rows) load(row0);
-  for (; row0 < a.rows; row0 += per * a.nblk) {
-    const int64_t row = row0 + sub;
-    float x[K][V], z[K][V], d[BWD ? K : 1][V];
+    for (int q = 0; q < U; ++q)
 #pragma unroll
-    for (int p = 0; p < K; ++p) {
-      unpack<IO, V>(rx[p], x[p]);
-      if (a.gate != kGateNone) unpack<IO, V>(rz[p], z[p]);
-      if (BWD) unpack<IO, V>(rd[p], d[p]);
-    }
-    if (row0 + per * a.nblk < a.rows) load(row0 + per * a.nblk);
-
-    // the group's values in u, centered
-    float u[K][V], s = 0.0f;
-#pragma unroll
-    for (int p = 0; p < K; ++p)
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        u[p][i] = a.gate == kGateFirst ? x[p][i] * act(a.activation, z[p][i]) : x[p][i];
-        s += u[p][i];
+      for (int p = 0; p < K; ++p) {
+        const int64_t row = r0 + q * rp + sub;
+        const bool ok = in_group[p] && row < a.rows;
+        rx[q][p] = fetch<IO, V>(a.x, row * a.x_row + ch[p], ok);
+        if (gate_kind != kGateNone) rz[q][p] = fetch<IO, V>(a.z, row * a.z_row + ch[p], ok);
+        if (BWD) rd[q][p] = fetch<IO, V>(a.dy, row * a.dy_row + ch[p], ok);
       }
-    if (a.center) {
-      // divided, not multiplied by a rounded reciprocal: a group of equal values keeps no residue to be blown up
-      const float mu = sum(s) / static_cast<float>(a.gs);
+  };
+  for (; row0 < a.rows; row0 += per * a.nblk) {
+    load(row0);
+    float x[U][K][V], z[U][K][V], d[BWD ? U : 1][K][V], gate[BWD ? U : 1][K][V], u[U][K][V], r[U];
+#pragma unroll
+    for (int q = 0; q < U; ++q)
+#pragma unroll
+      for (int p = 0; p < K; ++p) {
+        unpack<IO, V>(rx[q][p], x[q][p]);
+        if (gate_kind != kGateNone) unpack<IO, V>(rz[q][p], z[q][p]);
+        if (BWD) unpack<IO, V>(rd[q][p], d[q][p]);
+      }
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      // the group's values in u, centered
+      float s = 0.0f;
 #pragma unroll
       for (int p = 0; p < K; ++p)
 #pragma unroll
-        for (int i = 0; i < V; ++i) u[p][i] = in_group[p] ? u[p][i] - mu : 0.0f;
+        for (int i = 0; i < V; ++i) {
+          u[q][p][i] = x[q][p][i];
+          if (gate_kind == kGateFirst) {
+            float g;
+            if (BWD) {  // z becomes the derivative, the gate itself is kept too
+              z[q][p][i] = act_grad(a.activation, z[q][p][i], g);
+              gate[q][p][i] = g;
+            } else {
+              g = act(a.activation, z[q][p][i]);
+            }
+            u[q][p][i] *= g;
+          }
+          s += u[q][p][i];
+        }
+      if (a.center) {
+        // divided, not multiplied by a rounded reciprocal: a group of equal values keeps no residue to be blown up
+        const float mu = sum1(s) / static_cast<float>(a.gs);
+#pragma unroll
+        for (int p = 0; p < K; ++p)
+#pragma unroll
+          for (int i = 0; i < V; ++i) u[q][p][i] = in_group[p] ? u[q][p][i] - mu : 0.0f;
+      }
+      s = 0.0f;
+#pragma unroll
+      for (int p = 0; p < K; ++p)
+#pragma unroll
+        for (int i = 0; i < V; ++i) s = fmaf(u[q][p][i], u[q][p][i], s);
+      // 0 for the rows behind the last: with eps 0 their zeros would become NaN in the parameters' sums
+      s = sum1(s);
+      r[q] = row0 + q * rp + sub < a.rows ? __builtin_amdgcn_rsqf(fmaf(s, inv, a.eps)) : 0.0f;
     }
-    s = 0.0f;
-#pragma unroll
-    for (int p = 0; p < K; ++p)
-#pragma unroll
-      for (int i = 0; i < V; ++i) s = fmaf(u[p][i], u[p][i], s);
-    // 0 for the rows behind the last: with eps 0 their zeros would become NaN in the parameters' sums
-    s = sum(s);
-    const float r = row < a.rows ? __builtin_amdgcn_rsqf(fmaf(s, inv, a.eps)) : 0.0f;
 
-    const int64_t out = row * a.channels;
-    if (!BWD) {
 #pragma unroll
-      for (int p = 0; p < K; ++p) {
-        float y[V];
+    for (int q = 0; q < U; ++q) {
+      const int64_t row = row0 + q * rp + sub, out = row * a.channels;
+      if (!BWD) {
+#pragma unroll
+        for (int p = 0; p < K; ++p) {
+          float y[V];
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            y[i] = fmaf(u[q][p][i] * r[q], w[p][i], b[p][i]);
+            if (gate_kind == kGateAfter) y[i] *= act(a.activation, z[q][p][i]);
+            if (gate_kind == kGateNone) y[i] = act(a.activation, y[i]);
+          }
+          if (in_group[p] && row < a.rows) put<IO, V>(static_cast<T*>(a.out) + out + ch[p], y);
+        }
+        continue;
+      }
+      // d becomes dxh, and z the factor of dz (gate after: dz itself)
+      float m[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int p = 0; p < K; ++p)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          y[i] = fmaf(u[p][i] * r, w[p][i], b[p][i]);
-          if (a.gate == kGateAfter) y[i] *= act(a.activation, z[p][i]);
-          if (a.gate == kGateNone) y[i] = act(a.activation, y[i]);
+          const float xh = u[q][p][i] * r[q];
+          u[q][p][i] = xh;
+          float dn = d[q][p][i];
+          if (gate_kind == kGateAfter) {
+            const float n = fmaf(xh, w[p][i], b[p][i]);
+            float g;
+            const float da = act_grad(a.activation, z[q][p][i], g);
+            z[q][p][i] = dn * n * da;
+            dn *= g;
+          } else if (gate_kind == kGateNone) {
+            float g;
+            dn *= act_grad(a.activation, fmaf(xh, w[p][i], b[p][i]), g);
+          }
+          sw[p][i] = fmaf(dn, xh, sw[p][i]);
+          sb[p][i] += dn;
+          d[q][p][i] = dn * w[p][i];
+          m[0] += d[q][p][i];
+          m[1] = fmaf(d[q][p][i], xh, m[1]);
         }
-        if (in_group[p] && row < a.rows) put<IO, V>(static_cast<T*>(a.out) + out + ch[p], y);
-      }
-      continue;
-    }
-    // d becomes dxh, and z the factor of dz (gate after: dz itself)
-    float m1 = 0.0f, m2 = 0.0f;
+      sum(m);
+      const float m1 = a.center ? m[0] * inv : 0.0f, m2 = m[1] * inv;
 #pragma unroll
-    for (int p = 0; p < K; ++p)
+      for (int p = 0; p < K; ++p) {
+        float dx[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float xh = u[p][i] * r;
-        u[p][i] = xh;
-        float dn = d[p][i];
-        if (a.gate == kGateAfter) {
-          const float n = fmaf(xh, w[p][i], b[p][i]);
-          float g;
-          const float da = act_grad(a.activation, z[p][i], g);
-          z[p][i] = dn * n * da;
-          dn *= g;
-        } else if (a.gate == kGateNone) {
-          float g;
-          dn *= act_grad(a.activation, fmaf(xh, w[p][i], b[p][i]), g);
+        for (int i = 0; i < V; ++i) {
+          dx[i] = r[q] * (d[q][p][i] - m1 - u[q][p][i] * m2);
+          if (gate_kind == kGateFirst) {
+            z[q][p][i] *= dx[i] * x[q][p][i];
+            dx[i] *= gate[q][p][i];
+          }
         }
-        sw[p][i] = fmaf(dn, xh, sw[p][i]);
-        sb[p][i] += dn;
-        d[p][i] = dn * w[p][i];
-        m1 += d[p][i];
-        m2 = fmaf(d[p][i], xh, m2);
-      }
-    m1 = a.center ? sum(m1) * inv : 0.0f;
-    m2 = sum(m2) * inv;
-#pragma unroll
-    for (int p = 0; p < K; ++p) {
-      float dx[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        dx[i] = r * (d[p][i] - m1 - u[p][i] * m2);
-        if (a.gate == kGateFirst) {
-          float g;
-          const float da = act_grad(a.activation, z[p][i], g);
-          z[p][i] = dx[i] * x[p][i] * da;
-          dx[i] *= g;
+        if (in_group[p] && row < a.rows) {
+          put<IO, V>(static_cast<T*>(a.out) + out + ch[p], dx);
+          if (gate_kind != kGateNone) put<IO, V>(static_cast<T*>(a.dz) + out + ch[p], z[q][p]);
         }
-      }
-      if (in_group[p] && row < a.rows) {
-        put<IO, V>(static_cast<T*>(a.out) + out + ch[p], dx);
-        if (a.gate != kGateNone) put<IO, V>(static_cast<T*>(a.dz) + out + ch[p], z[p]);
       }
     }
   }
@@ -344,45 +407,52 @@ __global__ __launch_bounds__(WIDE ? 1024 : 64 * kWaves) void gnorm_kernel(const 
   }
 }
 
-// out[c] = sum over blocks of part[block][c]: 64 channels a workgroup, whose 16
-// waves take every 16th block.
+// out[c] = sum over blocks of part[block][c]: 16 channels a workgroup, whose 64
+// quarter waves take every 64th block, four at a time.
 __global__ __launch_bounds__(1024) void gnorm_sum_kernel(int32_t nblk, int32_t channels, const float* pw,
                                                          const float* pb, float* dw, float* db) {
-  __shared__ float red[16][64];
+  __shared__ float red[64][17];
   const float* part = blockIdx.y == 0 ? pw : pb;
   float* out = blockIdx.y == 0 ? dw : db;
   if (!out) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = blockIdx.x * 64 + lane;
-  float s = 0.0f;
+  const int l = threadIdx.x & 15, h = threadIdx.x >> 4;
+  const int c = blockIdx.x * 16 + l;
+  float s[4] = {};
   if (c < channels)
-    for (int j = wave; j < nblk; j += 16) s += part[static_cast<int64_t>(j) * channels + c];
-  red[wave][lane] = s;
+    for (int j = h; j < nblk; j += 256)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (j + 64 * k < nblk) s[k] += part[static_cast<int64_t>(j + 64 * k) * channels + c];
+  red[h][l] = (s[0] + s[1]) + (s[2] + s[3]);
   __syncthreads();
-  if (wave == 0 && c < channels) {
-    for (int j = 1; j < 16; ++j) s += red[j][lane];
-    out[c] = s;
+  // the 64 sums of a channel: 16 threads a channel, then 16 lanes together
+  const int cl = threadIdx.x >> 4, hl = threadIdx.x & 15;
+  if (cl < 16) {
+    float t = (red[hl][cl] + red[hl + 16][cl]) + (red[hl + 32][cl] + red[hl + 48][cl]);
+    t = lanes_sum(t, 16);
+    if (hl == 0 && blockIdx.x * 16 + cl < channels) out[blockIdx.x * 16 + cl] = t;
   }
 }
 
 // How a group is laid out over lanes.
 struct Layout {
-  int vec, k, threads;  // elements a piece (1: any alignment), pieces a lane, threads of a workgroup
+  int vec, k, u, threads;  // elements a piece (1: any alignment), pieces a lane, rows at a time, threads of a workgroup
   int ln, ln_log, gp, tiles, rp;
   bool wide;
 };
-Layout layout(int32_t channels, int32_t groups, int32_t io_dtype, bool can_vec) {
+Layout layout(int32_t channels, int32_t groups, int32_t io_dtype, bool can_vec, bool bwd) {
   Layout l{};
   const int gs = channels / groups, full = io_dtype == 0 ? 4 : 8;
   l.vec = can_vec && gs % full == 0 ? full : 1;
-  const int pieces = gs / l.vec, most = l.vec == 1 ? 16 : 4;  // pieces of a lane in one wave
+  const int pieces = gs / l.vec, most = l.vec == 1 ? 8 : 1;  // pieces of a lane in one wave
   l.wide = pieces > 64 * most;
   l.gp = 1;
   l.rp = 1;
+  l.u = 1;
   if (l.wide) {
-    l.k = 16 / l.vec;
-    l.threads = 256;
-    while (l.threads * l.k < pieces) l.threads *= 2;
+    // whole waves, of as few pieces a lane as 16 of them allow
+    l.k = l.vec == 1 ? (pieces <= 4096 ? 4 : 16) : pieces <= 1024 ? 1 : io_dtype == 0 ? 4 : 2;
+    l.threads = ((pieces + l.k - 1) / l.k + 63) / 64 * 64;
     l.ln = l.threads;
   } else {
     l.threads = 64 * kWaves;
@@ -392,7 +462,8 @@ Layout layout(int32_t channels, int32_t groups, int32_t io_dtype, bool can_vec) 
       ++l.ln_log;
     }
     l.k = (pieces + l.ln - 1) / l.ln;
-    if (l.vec == 1) l.k = l.k <= 2 ? 2 : l.k <= 8 ? 8 : 16;
+    if (l.vec == 1) l.k = l.k <= 2 ? 2 : 8;
+    if (l.vec > 1) l.u = bwd ? 2 : 4;
     // neighbouring groups of a row, as many as divide it evenly
     while (l.gp * 2 * l.ln <= 64 && groups % (l.gp * 2) == 0) l.gp *= 2;
     l.rp = 64 / (l.ln * l.gp);
@@ -401,38 +472,51 @@ Layout layout(int32_t channels, int32_t groups, int32_t io_dtype, bool can_vec) 
   return l;
 }
 
-// Workgroups that share the rows of a tile.
-int64_t blocks(const Layout& l, int64_t rows, bool bwd) {
-  const int64_t per = l.wide ? 1 : static_cast<int64_t>(kWaves) * l.rp;
+// Workgroups that share the rows of a tile, with as many turns for each. The
+// backward takes one round of what is resident, so that few partial sums are
+// left: by its registers 16 waves on a CU (float32: 24), or three workgroups
+// of four waves where a wave holds whole groups (16384 x 1536 bf16, one group,
+// three waves: 1280 workgroups 60 us, 1536 71 us, 768 69 us; twelve groups:
+// 768 workgroups 53 us, 1280 56 us).
+int64_t blocks(const Layout& l, int64_t rows, int32_t io_dtype, bool bwd) {
+  const int64_t per = l.wide ? 1 : static_cast<int64_t>(kWaves) * l.u * l.rp;
   const int64_t all = (rows + per - 1) / per;
-  const int64_t want = ((bwd ? 1024 : 8192) + l.tiles - 1) / l.tiles;
-  return all < want ? all : want;
+  const int waves = l.threads / 64, held = (io_dtype == 0 ? 24 : 16) / waves;
+  const int64_t slots = 256 * (!l.wide ? 3 : held > 1 ? held : 1);
+  const int64_t most = ((bwd ? slots : 16384) + l.tiles - 1) / l.tiles;
+  const int64_t turns = (all + most - 1) / most;
+  return (all + turns - 1) / turns;
 }
 
-template <int IO, int V, int K, bool WIDE>
-hipError_t launch_typed(const GnCall& c, const Layout& l, const GnArgs& a) {
+template <int IO, int V, int K, int UF, int UB, bool WIDE, int GATE>
+hipError_t launch_gate(const GnCall& c, const Layout& l, const GnArgs& a) {
   const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(l.tiles) * a.nblk)), block(l.threads);
   if (c.dy)
-    hipLaunchKernelGGL((gnorm_kernel<IO, V, K, WIDE, true>), grid, block, 0, c.stream, a);
+    hipLaunchKernelGGL((gnorm_kernel<IO, V, K, UB, WIDE, true, GATE>), grid, block, 0, c.stream, a);
   else
-    hipLaunchKernelGGL((gnorm_kernel<IO, V, K, WIDE, false>), grid, block, 0, c.stream, a);
+    hipLaunchKernelGGL((gnorm_kernel<IO, V, K, UF, WIDE, false, GATE>), grid, block, 0, c.stream, a);
   return hipGetLastError();
+}
+template <int IO, int V, int K, int UF, int UB, bool WIDE>
+hipError_t launch_typed(const GnCall& c, const Layout& l, const GnArgs& a) {
+  if (a.gate == kGateNone) return launch_gate<IO, V, K, UF, UB, WIDE, kGateNone>(c, l, a);
+  if (a.gate == kGateAfter) return launch_gate<IO, V, K, UF, UB, WIDE, kGateAfter>(c, l, a);
+  return launch_gate<IO, V, K, UF, UB, WIDE, kGateFirst>(c, l, a);
 }
 
 template <int IO>
 hipError_t launch_io(const GnCall& c, const Layout& l, const GnArgs& a) {
   constexpr int V = IO == 0 ? 4 : 8;
-  if (l.wide) return l.vec == 1 ? launch_typed<IO, 1, 16, true>(c, l, a) : launch_typed<IO, V, 16 / V, true>(c, l, a);
-  if (l.vec == 1) {
-    if (l.k == 2) return launch_typed<IO, 1, 2, false>(c, l, a);
-    return l.k == 8 ? launch_typed<IO, 1, 8, false>(c, l, a) : launch_typed<IO, 1, 16, false>(c, l, a);
+  if (l.wide) {
+    if (l.vec == 1)
+      return l.k == 4 ? launch_gate<IO, 1, 4, 1, 1, true, kGateAny>(c, l, a)
+                      : launch_gate<IO, 1, 16, 1, 1, true, kGateAny>(c, l, a);
+    return l.k == 1 ? launch_typed<IO, V, 1, 1, 1, true>(c, l, a)
+                    : launch_gate<IO, V, 16 / V, 1, 1, true, kGateAny>(c, l, a);
   }
-  switch (l.k) {
-    case 1: return launch_typed<IO, V, 1, false>(c, l, a);
-    case 2: return launch_typed<IO, V, 2, false>(c, l, a);
-    case 3: return launch_typed<IO, V, 3, false>(c, l, a);
-    default: return launch_typed<IO, V, 4, false>(c, l, a);
-  }
+  if (l.vec == 1)
+    return l.k == 2 ? launch_typed<IO, 1, 2, 1, 1, false>(c, l, a) : launch_gate<IO, 1, 8, 1, 1, false, kGateAny>(c, l, a);
+  return launch_typed<IO, V, 1, 4, 2, false>(c, l, a);
 }
 
 }  // namespace
@@ -440,8 +524,8 @@ hipError_t launch_io(const GnCall& c, const Layout& l, const GnArgs& a) {
 size_t gn_part_floats(int64_t rows, int32_t channels, int32_t groups, int32_t io_dtype, int sums) {
   if (sums == 0) return 0;
   // the call may take either layout, by the alignment of its tensors
-  const int64_t v = blocks(layout(channels, groups, io_dtype, true), rows, true);
-  const int64_t s = blocks(layout(channels, groups, io_dtype, false), rows, true);
+  const int64_t v = blocks(layout(channels, groups, io_dtype, true, true), rows, io_dtype, true);
+  const int64_t s = blocks(layout(channels, groups, io_dtype, false, true), rows, io_dtype, true);
   return static_cast<size_t>(v > s ? v : s) * channels * sums;
 }
 
@@ -450,7 +534,7 @@ hipError_t launch_gnorm(const GnCall& c) {
   auto fits = [&](const void* p, int64_t row) { return (reinterpret_cast<uintptr_t>(p) % 16) == 0 && row % full == 0; };
   const bool can_vec = fits(c.x, c.x_row) && fits(c.out, c.channels) && (!c.z || fits(c.z, c.z_row)) &&
                        (!c.dy || fits(c.dy, c.dy_row)) && (!c.dz || fits(c.dz, c.channels));
-  const Layout l = layout(c.channels, c.groups, c.io_dtype, can_vec);
+  const Layout l = layout(c.channels, c.groups, c.io_dtype, can_vec, c.dy != nullptr);
   GnArgs a{};
   a.rows = c.rows;
   a.x_row = c.x_row;
@@ -462,7 +546,7 @@ hipError_t launch_gnorm(const GnCall& c) {
   a.ln_log = l.ln_log;
   a.gp = l.gp;
   a.tiles = l.tiles;
-  a.nblk = static_cast<int32_t>(blocks(l, c.rows, c.dy != nullptr));
+  a.nblk = static_cast<int32_t>(blocks(l, c.rows, c.io_dtype, c.dy != nullptr));
   a.activation = c.activation;
   a.gate = c.gate;
   a.center = c.center;
@@ -479,7 +563,7 @@ hipError_t launch_gnorm(const GnCall& c) {
   a.pb = c.dbias ? c.part + (c.dweight ? n : 0) : nullptr;
   hipError_t e = c.io_dtype == 0 ? launch_io<0>(c, l, a) : launch_io<1>(c, l, a);
   if (e != hipSuccess || (!a.pw && !a.pb)) return e;
-  hipLaunchKernelGGL(gnorm_sum_kernel, dim3(static_cast<unsigned>((c.channels + 63) / 64), 2), dim3(1024), 0, c.stream,
+  hipLaunchKernelGGL(gnorm_sum_kernel, dim3(static_cast<unsigned>((c.channels + 15) / 16), 2), dim3(1024), 0, c.stream,
                      a.nblk, c.channels, a.pw, a.pb, c.dweight, c.dbias);
   return hipGetLastError();
 }

@@ -854,7 +854,12 @@ size_t state_floats(const LaPlan& p, int32_t batch, int32_t nheads, int32_t kd, 
 LaPlan la_plan(int32_t batch, int32_t seqlen, int32_t nheads, int32_t d_k, int32_t d_v, int32_t nroles) {
   const int32_t nchunks = (seqlen + kC - 1) / kC;
   const int64_t groups = static_cast<int64_t>(nroles) * batch * nheads * ((d_v + kVS - 1) / kVS);
-  const int64_t want = (512 + groups - 1) / groups, most = nchunks / 4 > 1 ? nchunks / 4 : 1;
+  // One workgroup per CU is resident where the heads are wide, three where the
+  // state alone is summed. Splitting reads k and v once more, so heads enough
+  // for five CUs in eight go unsplit (8 x 2048, 12 heads of 128, 192
+  // workgroups: 69 us, 107 split in four), and fewer are split into three
+  // rounds (1 x 65536, 24 workgroups: 357 us in 32 segments, 436 in 8).
+  const int64_t want = groups >= 160 ? 1 : 768 / groups, most = nchunks / 4 > 1 ? nchunks / 4 : 1;
   const int32_t nseg = static_cast<int32_t>(want < most ? want : most);
   LaPlan p;
   p.seg_chunks = (nchunks + nseg - 1) / nseg;

@@ -37,11 +37,10 @@ def load():
     return lib
 
 
-def _like(t, x, name, dtype, device):
-    t, row = _rows(t, name, dtype, device, t.dim() - 1 if isinstance(t, torch.Tensor) and t.dim() else 1, 1)
-    if t.shape != x.shape:
-        raise _b.MambaScanError(2, "%s must be %s (got %s)" % (name, list(x.shape), list(t.shape)))
-    return t, row
+def _like(t, shape, name, dtype, device):
+    if isinstance(t, torch.Tensor) and t.shape != shape:
+        raise _b.MambaScanError(2, "%s must be %s (got %s)" % (name, list(shape), list(t.shape)))
+    return _rows(t, name, dtype, device, len(shape) - 1, 1)
 
 
 def _param(t, name, device, channels):
@@ -55,26 +54,26 @@ def _param(t, name, device, channels):
 
 
 def _common(x, weight, bias, groups, z, activation, gate_first, center, eps):
-    io = _io_of(x, "x")
-    if x.dim() < 1:
-        raise _b.MambaScanError(2, "x must be [..., channels]")
-    if activation not in _ACT:
+    """The checked tensors, and the entry points' common arguments."""
+    io, dtype, dev = _io_of(x, "x")
+    act = _ACT.get(activation)
+    if act is None:
         raise _b.MambaScanError(2, "activation must be one of %s (got %r)" % (sorted(_ACT), activation))
     if gate_first and z is None:
         raise _b.MambaScanError(1, "gate_first needs z")
-    dtype, dev = x.dtype, x.device
-    channels = x.shape[-1]
-    x, xs = _rows(x, "x", dtype, dev, x.dim() - 1, 1)
-    zs, zp = 0, 0
+    shape = x.shape
+    if len(shape) < 1:
+        raise _b.MambaScanError(2, "x must be [..., channels]")
+    channels = shape[-1]
+    x, xp, xs = _rows(x, "x", dtype, dev, len(shape) - 1, 1)
+    gate = zp = zs = 0
     if z is not None:
-        z, zs = _like(z, x, "z", dtype, dev)
-        zp = z.data_ptr()
+        z, zp, zs = _like(z, shape, "z", dtype, dev)
+        gate = 2 if gate_first else 1
     weight, wp = _param(weight, "weight", dev, channels)
     bias, bp = _param(bias, "bias", dev, channels)
     rows = x.numel() // channels if channels else 0
-    gate = 0 if z is None else 2 if gate_first else 1
-    args = (rows, channels, groups, io, _ACT[activation], gate, 1 if center else 0, eps, x.data_ptr(), xs, zp, zs, wp, bp)
-    return x, args, (z, weight, bias)
+    return dev, x, (rows, channels, groups, io, act, gate, 1 if center else 0, eps, xp, xs, zp, zs, wp, bp), (z, weight, bias)
 
 
 def group_norm_fwd(x, weight, bias, groups, z=None, *, eps=1e-5, activation="silu", gate_first=False, center=True,
@@ -83,13 +82,10 @@ def group_norm_fwd(x, weight, bias, groups, z=None, *, eps=1e-5, activation="sil
     plus bias ([channels] float32, or None), with an activation ("silu", "sigmoid" or "none"): of the gate z (like x),
     which multiplies the result or, with gate_first, x before its norm; without z, of the result itself. center=False
     takes no mean off (RMS). x and z may be columns of a wider tensor; they are read in place. Returns y like x."""
-    lib = load()
-    x, args, keep = _common(x, weight, bias, groups, z, activation, gate_first, center, eps)
-    if out is not None:
-        y = check_out(out, "out", x.shape, x.dtype, x.device)
-    else:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    launch(x.device, "mamba_gnorm_fwd", lib, lib.mamba_gnorm_fwd, *args, y.data_ptr())
+    lib = _lib or load()
+    dev, x, args, keep = _common(x, weight, bias, groups, z, activation, gate_first, center, eps)
+    y = x.new_empty(x.shape) if out is None else check_out(out, "out", x.shape, x.dtype, x.device)
+    launch(dev, "mamba_gnorm_fwd", lib, lib.mamba_gnorm_fwd, *args, y.data_ptr())
     return y
 
 
@@ -99,25 +95,27 @@ def group_norm_bwd(x, weight, bias, groups, dy, z=None, *, eps=1e-5, activation=
 
     Returns a dict: dx (and dz, where z is given) like x, and dweight, dbias ([channels] float32) where weight and
     bias are given."""
-    lib = load()
-    x, args, (z, weight, bias) = _common(x, weight, bias, groups, z, activation, gate_first, center, eps)
-    dev = x.device
-    dy, dys = _like(dy, x, "dy", x.dtype, dev)
-    grads = {"dx": torch.empty(x.shape, dtype=x.dtype, device=dev)}
+    lib = _lib or load()
+    dev, x, args, (z, weight, bias) = _common(x, weight, bias, groups, z, activation, gate_first, center, eps)
+    shape = x.shape
+    dy, dyp, dys = _like(dy, shape, "dy", x.dtype, dev)
+    grads = {"dx": x.new_empty(shape)}
     dz = dw = db = 0
     if z is not None:
-        grads["dz"] = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        grads["dz"] = x.new_empty(shape)
         dz = grads["dz"].data_ptr()
     if weight is not None:
-        grads["dweight"] = torch.empty(weight.shape, dtype=_F32, device=dev)
+        grads["dweight"] = torch.empty_like(weight)
         dw = grads["dweight"].data_ptr()
     if bias is not None:
-        grads["dbias"] = torch.empty(bias.shape, dtype=_F32, device=dev)
+        grads["dbias"] = torch.empty_like(bias)
         db = grads["dbias"].data_ptr()
-    need = lib.mamba_gnorm_bwd_workspace_bytes(*args[:4], 1 if dw else 0, 1 if db else 0)
-    ws, ws_bytes, keep = scratch(workspace, need, dev)
-    launch(dev, "mamba_gnorm_bwd", lib, lib.mamba_gnorm_bwd, *args, dy.data_ptr(), dys, grads["dx"].data_ptr(), dz, dw,
-           db, ws, ws_bytes)
+    need = 0
+    if dw or db:
+        need = lib.mamba_gnorm_bwd_workspace_bytes(*args[:4], 1 if dw else 0, 1 if db else 0)
+    ws, ws_bytes, keep = scratch(workspace, need, x)
+    launch(dev, "mamba_gnorm_bwd", lib, lib.mamba_gnorm_bwd, *args, dyp, dys, grads["dx"].data_ptr(), dz, dw, db, ws,
+           ws_bytes)
     return grads
 
 

@@ -9,6 +9,7 @@ device addresses plus torch's current HIP stream to the entry points of
 include/mamba_linattn.h. The arithmetic is all in the library's kernels.
 """
 import ctypes
+import math
 
 import torch
 
@@ -43,24 +44,32 @@ def load():
     return lib
 
 
+# The current stream's address without the wrapper objects of torch.cuda (a
+# call of one token takes few microseconds on the GPU).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _tensor(t, name, dtype, device):
+    """Check that t is a tensor of `dtype` on GPU number `device`."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise _b.MambaScanError(7, "%s must be on the GPU (got %s); there is no CPU path" % (name, t.device))
     if t.dtype != dtype:
         raise TypeError("%s must be %s (got %s)" % (name, dtype, t.dtype))
-    if t.device != device:
-        raise _b.MambaScanError(7, "%s is on %s, expected %s" % (name, t.device, device))
+    if t.get_device() != device:
+        raise _b.MambaScanError(7, "%s is on %s, expected cuda:%d" % (name, t.device, device))
     return t
 
 
 def _io_of(x, name):
+    """(io code, dtype, GPU number) that a call's first io tensor sets for the others."""
     if not isinstance(x, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if x.dtype not in _IO:
+    io = _IO.get(x.dtype)
+    if io is None:
         raise TypeError("io tensors must be float32 or bfloat16 (got %s)" % x.dtype)
-    return _IO[x.dtype]
+    return io, x.dtype, x.get_device() if x.is_cuda else -1
 
 
 def row_stride(shape, strides, nrow):
@@ -86,82 +95,77 @@ def row_stride(shape, strides, nrow):
 
 
 def _rows(t, name, dtype, device, nrow, align):
-    """(the tensor or a contiguous copy of it, its row stride), readable in place by the library."""
+    """(the tensor or a contiguous copy of it, its address, its row stride), readable in place by the library."""
     t = _tensor(t, name, dtype, device)
-    if t.is_contiguous():
-        if t.data_ptr() % align:
-            t = t.clone()
-        width = 1
-        for n in t.shape[nrow:]:
-            width *= n
-        return t, width
-    step = row_stride(t.shape, t.stride(), nrow)
-    if step and not t.data_ptr() % align and not step * t.element_size() % align:
-        return t, step
-    t = t.contiguous()
-    width = 1
-    for n in t.shape[nrow:]:
-        width *= n
-    return t, width
+    at = t.data_ptr()
+    shape = t.shape
+    if not at % align:
+        if t.is_contiguous():
+            return t, at, math.prod(shape[nrow:])
+        step = row_stride(shape, t.stride(), nrow)
+        if step and not step * t.element_size() % align:
+            return t, at, step
+    t = t.clone(memory_format=torch.contiguous_format)
+    return t, t.data_ptr(), math.prod(shape[nrow:])
 
 
 def _f32(t, name, device, shape):
+    """(a float32 tensor of `shape`, contiguous and 16-byte aligned, its address); (None, 0) for None."""
     if t is None:
-        return None
+        return None, 0
     t = _tensor(t, name, _F32, device)
     if t.shape != shape:
         raise _b.MambaScanError(2, "%s must be %s (got %s)" % (name, list(shape), list(t.shape)))
-    t = t.contiguous()
-    return t if t.data_ptr() % 16 == 0 else t.clone()
+    at = t.data_ptr()
+    if at % 16 or not t.is_contiguous():
+        t = t.clone(memory_format=torch.contiguous_format)
+        at = t.data_ptr()
+    return t, at
 
 
 def _ids(seq_idx, device, batch, seqlen):
     if seq_idx is None:
-        return None
+        return None, 0
     if isinstance(seq_idx, torch.Tensor) and seq_idx.dtype in (torch.int64, torch.int16, torch.int8, torch.uint8):
         seq_idx = seq_idx.to(torch.int32)
     seq_idx = _tensor(seq_idx, "seq_idx", torch.int32, device)
     if seq_idx.shape != (batch, seqlen):
         raise _b.MambaScanError(2, "seq_idx must be [%d, %d]" % (batch, seqlen))
-    return seq_idx.contiguous()
-
-
-def _addr(t):
-    return 0 if t is None else t.data_ptr()
-
-
-def _check(lib, status, what):
-    if status != 0:
-        _b._check(lib, status, what)
+    seq_idx = seq_idx.contiguous()
+    return seq_idx, seq_idx.data_ptr()
 
 
 def launch(device, what, lib, fn, *args):
-    """Call an entry point with `device` current and its current stream as the last argument."""
-    if device.index == torch.cuda.current_device():
-        _check(lib, fn(*args, torch.cuda.current_stream(device).cuda_stream), what)
-    else:
+    """Call an entry point with GPU number `device` current and its current stream as the last argument."""
+    if device != torch.cuda.current_device():
         with torch.cuda.device(device):
-            _check(lib, fn(*args, torch.cuda.current_stream(device).cuda_stream), what)
+            return launch(device, what, lib, fn, *args)
+    stream = _raw_stream(device) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
+    status = fn(*args, stream)
+    if status:
+        _b._check(lib, status, what)
 
 
-def scratch(workspace, need, device):
-    """(address, bytes, tensor) of the caller's workspace or, where it is None, of a new one of `need` bytes."""
-    workspace = check_workspace(workspace, device)
+def scratch(workspace, need, x):
+    """(address, bytes, tensor) of the caller's workspace or, where it is None, of a new one of `need` bytes; on the
+    device of x."""
     if workspace is None:
         if not need:
             return 0, 0, None
-        workspace = torch.empty(need, device=device, dtype=torch.uint8)
+        workspace = x.new_empty(need, dtype=torch.uint8)
+        return workspace.data_ptr(), need, workspace
+    workspace = check_workspace(workspace, x.device)
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
-def _sizes(q, k, v, name_v="v"):
+def _sizes(q, k, v):
     if q.dim() != 4 or v.dim() != 4:
         raise _b.MambaScanError(2, "q and k must be [batch, seqlen, ngroups, d_k] and v [batch, seqlen, nheads, d_v]")
-    if k.shape != q.shape or v.shape[:2] != q.shape[:2]:
-        raise _b.MambaScanError(2, "shape mismatch between q %s, k %s and v %s" % (tuple(q.shape), tuple(k.shape),
-                                                                                 tuple(v.shape)))
-    batch, seqlen, ngroups, d_k = q.shape
-    return batch, seqlen, v.shape[2], ngroups, d_k, v.shape[3]
+    qs, vs = q.shape, v.shape
+    if k.shape != qs or vs[:2] != qs[:2]:
+        raise _b.MambaScanError(2, "shape mismatch between q %s, k %s and v %s" % (tuple(qs), tuple(k.shape), tuple(vs)))
+    batch, seqlen, ngroups, d_k = qs
+    return batch, seqlen, vs[2], ngroups, d_k, vs[3]
 
 
 def lin_attn_workspace_bytes(batch, seqlen, nheads, ngroups, d_k, d_v, dtype, backward=False):
@@ -178,25 +182,25 @@ def lin_attn_fwd(q, k, v, log_decay, state=None, *, scale=None, seq_idx=None, ou
     None; seq_idx [batch, seqlen] integer document ids or None (packed documents: the state restarts from zero
     wherever the id changes). q, k and v may be columns of one wider tensor; they are read in place.
     Returns (y like v, final state or None)."""
-    lib = load()
-    io = _io_of(q, "q")
-    dtype, dev = q.dtype, q.device
-    q, qs = _rows(q, "q", dtype, dev, 2, 16)
-    k, ks = _rows(k, "k", dtype, dev, 2, 16)
-    v, vs = _rows(v, "v", dtype, dev, 2, 16)
+    lib = _lib or load()
+    io, dtype, dev = _io_of(q, "q")
+    q, qp, qs = _rows(q, "q", dtype, dev, 2, 16)
+    k, kp, ks = _rows(k, "k", dtype, dev, 2, 16)
+    v, vp, vs = _rows(v, "v", dtype, dev, 2, 16)
     batch, seqlen, nheads, ngroups, d_k, d_v = sizes = _sizes(q, k, v)
-    log_decay = _f32(log_decay, "log_decay", dev, (nheads,))
-    state = _f32(state, "state", dev, (batch, nheads, d_v, d_k))
-    seq_idx = _ids(seq_idx, dev, batch, seqlen)
-    y = check_out(out, "out", v.shape, dtype, dev) if out is not None else torch.empty(v.shape, dtype=dtype, device=dev)
+    state_shape = (batch, nheads, d_v, d_k)
+    log_decay, gp = _f32(log_decay, "log_decay", dev, (nheads,))
+    state, sp = _f32(state, "state", dev, state_shape)
+    seq_idx, ip = _ids(seq_idx, dev, batch, seqlen)
+    y = q.new_empty(v.shape) if out is None else check_out(out, "out", v.shape, dtype, q.device)
     if state_out is not None:
-        check_out(state_out, "state_out", (batch, nheads, d_v, d_k), _F32, dev)
+        check_out(state_out, "state_out", state_shape, _F32, q.device)
     elif return_state:
-        state_out = torch.empty(batch, nheads, d_v, d_k, device=dev, dtype=_F32)
-    ws, ws_bytes, keep = scratch(workspace, lib.mamba_linattn_fwd_workspace_bytes(*sizes, io), dev)
+        state_out = q.new_empty(state_shape, dtype=_F32)
+    ws, ws_bytes, keep = scratch(workspace, lib.mamba_linattn_fwd_workspace_bytes(*sizes, io), q)
     launch(dev, "mamba_linattn_fwd", lib, lib.mamba_linattn_fwd, *sizes, io, d_k ** -0.5 if scale is None else scale,
-           q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _addr(seq_idx), _addr(log_decay), _addr(state),
-           y.data_ptr(), _addr(state_out), ws, ws_bytes)
+           qp, qs, kp, ks, vp, vs, ip, gp, sp, y.data_ptr(), 0 if state_out is None else state_out.data_ptr(), ws,
+           ws_bytes)
     return y, state_out
 
 
@@ -206,29 +210,30 @@ def lin_attn_bwd(q, k, v, log_decay, dy, state=None, dstate=None, *, scale=None,
 
     Returns a dict: dq, dk, dv (dtype and shape of q, k, v; dq and dk are summed over the heads of a group) and,
     where a state is given, dstate (float32, its gradient). The decays are constants: they get no gradient."""
-    lib = load()
-    io = _io_of(q, "q")
-    dtype, dev = q.dtype, q.device
-    q, qs = _rows(q, "q", dtype, dev, 2, 16)
-    k, ks = _rows(k, "k", dtype, dev, 2, 16)
-    v, vs = _rows(v, "v", dtype, dev, 2, 16)
-    dy, dys = _rows(dy, "dy", dtype, dev, 2, 16)
+    lib = _lib or load()
+    io, dtype, dev = _io_of(q, "q")
+    q, qp, qs = _rows(q, "q", dtype, dev, 2, 16)
+    k, kp, ks = _rows(k, "k", dtype, dev, 2, 16)
+    v, vp, vs = _rows(v, "v", dtype, dev, 2, 16)
+    dy, dyp, dys = _rows(dy, "dy", dtype, dev, 2, 16)
     batch, seqlen, nheads, ngroups, d_k, d_v = sizes = _sizes(q, k, v)
     if dy.shape != v.shape:
         raise _b.MambaScanError(2, "dy must be %s (got %s)" % (list(v.shape), list(dy.shape)))
-    log_decay = _f32(log_decay, "log_decay", dev, (nheads,))
-    state = _f32(state, "state", dev, (batch, nheads, d_v, d_k))
-    dstate = _f32(dstate, "dstate", dev, (batch, nheads, d_v, d_k))
-    seq_idx = _ids(seq_idx, dev, batch, seqlen)
-    grads = {"dq": torch.empty(q.shape, dtype=dtype, device=dev), "dk": torch.empty(k.shape, dtype=dtype, device=dev),
-             "dv": torch.empty(v.shape, dtype=dtype, device=dev)}
+    state_shape = (batch, nheads, d_v, d_k)
+    log_decay, gp = _f32(log_decay, "log_decay", dev, (nheads,))
+    state, sp = _f32(state, "state", dev, state_shape)
+    dstate, dsp = _f32(dstate, "dstate", dev, state_shape)
+    seq_idx, ip = _ids(seq_idx, dev, batch, seqlen)
+    dq, dk, dv = q.new_empty(q.shape), q.new_empty(q.shape), q.new_empty(v.shape)
+    grads = {"dq": dq, "dk": dk, "dv": dv}
+    dsi = 0
     if state is not None:
-        grads["dstate"] = torch.empty(state.shape, dtype=_F32, device=dev)
-    ws, ws_bytes, keep = scratch(workspace, lib.mamba_linattn_bwd_workspace_bytes(*sizes, io), dev)
+        grads["dstate"] = q.new_empty(state_shape, dtype=_F32)
+        dsi = grads["dstate"].data_ptr()
+    ws, ws_bytes, keep = scratch(workspace, lib.mamba_linattn_bwd_workspace_bytes(*sizes, io), q)
     launch(dev, "mamba_linattn_bwd", lib, lib.mamba_linattn_bwd, *sizes, io, d_k ** -0.5 if scale is None else scale,
-           q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _addr(seq_idx), _addr(log_decay), _addr(state),
-           dy.data_ptr(), dys, _addr(dstate), grads["dq"].data_ptr(), grads["dk"].data_ptr(), grads["dv"].data_ptr(),
-           _addr(grads.get("dstate")), ws, ws_bytes)
+           qp, qs, kp, ks, vp, vs, ip, gp, sp, dyp, dys, dsp, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dsi, ws,
+           ws_bytes)
     return grads
 
 
@@ -236,31 +241,32 @@ def lin_attn_step(q, k, v, log_decay, state, *, scale=None, inplace=False, out=N
     """One token: q, k [batch, ngroups, d_k], v [batch, nheads, d_v], state [batch, nheads, d_v, d_k] float32
     (required). Functional by default (a new state is returned); with inplace=True the given state is updated and
     returned. Returns (y like v, state)."""
-    lib = load()
-    io = _io_of(q, "q")
-    dtype, dev = q.dtype, q.device
+    lib = _lib or load()
+    io, dtype, dev = _io_of(q, "q")
     es = q.element_size()
-    q, qs = _rows(q, "q", dtype, dev, 1, es)
-    k, ks = _rows(k, "k", dtype, dev, 1, es)
-    v, vs = _rows(v, "v", dtype, dev, 1, es)
+    q, qp, qs = _rows(q, "q", dtype, dev, 1, es)
+    k, kp, ks = _rows(k, "k", dtype, dev, 1, es)
+    v, vp, vs = _rows(v, "v", dtype, dev, 1, es)
     if state is None:
         raise _b.MambaScanError(1, "lin_attn_step needs a state")
     if q.dim() != 3 or v.dim() != 3:
         raise _b.MambaScanError(2, "q and k must be [batch, ngroups, d_k] and v [batch, nheads, d_v]")
-    if k.shape != q.shape or v.shape[0] != q.shape[0]:
-        raise _b.MambaScanError(2, "shape mismatch between q %s, k %s and v %s" % (tuple(q.shape), tuple(k.shape),
-                                                                                 tuple(v.shape)))
-    batch, ngroups, d_k = q.shape
-    nheads, d_v = v.shape[1:]
-    log_decay = _f32(log_decay, "log_decay", dev, (nheads,))
+    q_shape, v_shape = q.shape, v.shape
+    if k.shape != q_shape or v_shape[0] != q_shape[0]:
+        raise _b.MambaScanError(2, "shape mismatch between q %s, k %s and v %s" % (tuple(q_shape), tuple(k.shape),
+                                                                                 tuple(v_shape)))
+    batch, ngroups, d_k = q_shape
+    nheads, d_v = v_shape[1:]
+    state_shape = (batch, nheads, d_v, d_k)
+    log_decay, gp = _f32(log_decay, "log_decay", dev, (nheads,))
     if inplace:
-        check_out(state, "state", (batch, nheads, d_v, d_k), _F32, dev)
-        new = state
+        new = check_out(state, "state", state_shape, _F32, q.device)
+        sp = np = state.data_ptr()
     else:
-        state = _f32(state, "state", dev, (batch, nheads, d_v, d_k))
-        new = torch.empty(state.shape, dtype=_F32, device=dev)
-    y = check_out(out, "out", v.shape, dtype, dev) if out is not None else torch.empty(v.shape, dtype=dtype, device=dev)
+        state, sp = _f32(state, "state", dev, state_shape)
+        new = q.new_empty(state_shape, dtype=_F32)
+        np = new.data_ptr()
+    y = q.new_empty(v_shape) if out is None else check_out(out, "out", v_shape, dtype, q.device)
     launch(dev, "mamba_linattn_step", lib, lib.mamba_linattn_step, batch, nheads, ngroups, d_k, d_v, io,
-           d_k ** -0.5 if scale is None else scale, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
-           _addr(log_decay), _addr(state), y.data_ptr(), _addr(new))
+           d_k ** -0.5 if scale is None else scale, qp, qs, kp, ks, vp, vs, gp, sp, y.data_ptr(), np)
     return y, new
