@@ -27,6 +27,11 @@
 // Both tasks of a chunk run at once, one wave of each on a SIMD, and with K, V
 // and S in LDS twice there is one barrier to a chunk. K and V come through
 // registers two chunks ahead, Q straight into the lanes that multiply it.
+//
+// float32 io runs on the bfloat16 matrix cores as well, sixteen times as fast
+// as the float32 ones: every operand is the sum of three bfloat16 parts of 8
+// significant bits each, which hold a float32 whole, and a product takes the
+// six products of parts that reach above 2^-24 of it.
 #include <type_traits>
 
 #include "linattn_internal.h"
@@ -56,88 +61,105 @@ __device__ __forceinline__ float power(float g2, int n) {
   return n == 0 ? 1.0f : exp2_hw(static_cast<float>(n) * g2);
 }
 
-// Element j of a fragment as float32.
-__device__ __forceinline__ float frag_get(const Frag<1>& f, int j) { return static_cast<float>(f.v[j]); }
-__device__ __forceinline__ float frag_get(const Frag<0>& f, int j) { return j < 4 ? f.lo[j & 3] : f.hi[j & 3]; }
-
-// Zero the k-values of a lane's eight that lie below `first`.
-__device__ __forceinline__ Frag<1> frag_from(const Frag<1>& f, int first) {
-  u4 v = __builtin_bit_cast(u4, f.v);
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    v[j] &= (2 * j >= first ? 0xFFFFu : 0u) | (2 * j + 1 >= first ? 0xFFFF0000u : 0u);
-  return Frag<1>{__builtin_bit_cast(bf8, v)};
-}
-__device__ __forceinline__ Frag<0> frag_from(const Frag<0>& f, int first) {
-  Frag<0> r = f;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (j < first) r.lo[j] = 0.0f;
-    if (4 + j < first) r.hi[j] = 0.0f;
-  }
-  return r;
-}
-
-// The A operand of S Q^T from two neighbouring S^T tiles: 8 consecutive
-// k-elements, of which the first tile has the upper four where g is odd.
+// 8 k-values of a matrix-core operand, each the sum of N bfloat16 parts.
+template <int N>
+struct Parts {
+  bf8 p[N];
+};
+// An operand of the io type: bfloat16 is one part, float32 three.
 template <int IO>
-__device__ __forceinline__ Frag<IO> state_frag(f4 even, f4 odd, int g);
-template <>
-__device__ __forceinline__ Frag<1> state_frag<1>(f4 even, f4 odd, int g) {
-  const u4 v = __builtin_bit_cast(u4, frag_regs<1>(even, odd).v);
-  const bool up = g & 1;
-  const u4 w = {up ? v.z : v.x, up ? v.w : v.y, up ? v.x : v.z, up ? v.y : v.w};
-  return Frag<1>{__builtin_bit_cast(bf8, w)};
-}
-template <>
-__device__ __forceinline__ Frag<0> state_frag<0>(f4 even, f4 odd, int g) {
-  return g & 1 ? Frag<0>{odd, even} : Frag<0>{even, odd};
-}
+using Op = Parts<IO == 1 ? 1 : 3>;
 
-// The weighted values w V as matrix-core operands. The state is kept and
-// returned in float32, so for bfloat16 io the products w v (24 significant
-// bits) are split into bfloat16 parts, each the rounded rest of those before
-// it, and multiplied once for each: three parts hold all 24 bits. Where the
-// state is not returned, only y sees it, rounded to bfloat16 itself, and two
-// parts (16 bits) do; one would double the rounding that y gets.
-template <int IO>
-struct Weighted;
-template <>
-struct Weighted<1> {
-  static constexpr int kParts = 3;
-  Frag<1> part[3];
-  __device__ __forceinline__ void set(const float (&x)[8], bool three) {
-    float r[8], bad = 0.0f;
+// Each part is the rounded rest of those before it.
+template <int N>
+__device__ __forceinline__ Parts<N> split(const float (&x)[8]) {
+  Parts<N> o;
+  float r[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) r[j] = x[j];
+#pragma unroll
+  for (int p = 0; p < N; ++p)
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      r[j] = x[j];
-      bad = fmaf(x[j], 0.0f, bad);
+      const __bf16 h = static_cast<__bf16>(r[j]);
+      o.p[p][j] = h;
+      if (p + 1 < N) r[j] -= static_cast<float>(h);
     }
-    const bool inf = __any(bad != 0.0f);  // an infinity or NaN is whole in its first part
+  return o;
+}
+// The same of four values, two to a word.
+template <int N>
+__device__ __forceinline__ void split4(f4 x, u2 (&o)[N]) {
+  typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
 #pragma unroll
-    for (int p = 0; p < 3; ++p) {
-      if (p == 2 && !three) break;
+  for (int p = 0; p < N; ++p) {
+    const bf4 h = {static_cast<__bf16>(x[0]), static_cast<__bf16>(x[1]), static_cast<__bf16>(x[2]),
+                   static_cast<__bf16>(x[3])};
+    o[p] = __builtin_bit_cast(u2, h);
+    if (p + 1 < N) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const __bf16 h = static_cast<__bf16>(r[j]);
-        part[p].v[j] = h;
-        r[j] -= static_cast<float>(h);
-      }
-      if (inf) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) r[j] = r[j] == r[j] ? r[j] : 0.0f;
-      }
+      for (int r = 0; r < 4; ++r) x[r] -= static_cast<float>(h[r]);
     }
   }
-};
-template <>
-struct Weighted<0> {
-  static constexpr int kParts = 1;
-  Frag<0> part[1];
-  __device__ __forceinline__ void set(const float (&x)[8], bool) {
-    part[0] = Frag<0>{f4{x[0], x[1], x[2], x[3]}, f4{x[4], x[5], x[6], x[7]}};
+}
+// Element j as float32.
+template <int N>
+__device__ __forceinline__ float get(const Parts<N>& f, int j) {
+  float v = static_cast<float>(f.p[N - 1][j]);
+#pragma unroll
+  for (int p = N - 2; p >= 0; --p) v += static_cast<float>(f.p[p][j]);
+  return v;
+}
+// Zero the k-values of a lane's eight that lie below `first`.
+template <int N>
+__device__ __forceinline__ Parts<N> from_first(const Parts<N>& f, int first) {
+  Parts<N> o;
+#pragma unroll
+  for (int p = 0; p < N; ++p) {
+    u4 v = __builtin_bit_cast(u4, f.p[p]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[j] &= (2 * j >= first ? 0xFFFFu : 0u) | (2 * j + 1 >= first ? 0xFFFF0000u : 0u);
+    o.p[p] = __builtin_bit_cast(bf8, v);
   }
-};
+  return o;
+}
+// acc[i] += a[i] b over the pairs of parts that matter, the smallest first, and
+// each pair for all i in turn: consecutive products do not wait for each other.
+template <int M, int NA, int NB>
+__device__ __forceinline__ void mma_each(f4* acc, const Parts<NA> (&a)[M], const Parts<NB>& b) {
+  constexpr int kMost = (NA > NB ? NA : NB) - 1;
+#pragma unroll
+  for (int o = kMost; o >= 0; --o)
+#pragma unroll
+    for (int pa = 0; pa < NA; ++pa) {
+      const int pb = o - pa;
+      if (pb < 0 || pb >= NB) continue;
+#pragma unroll
+      for (int i = 0; i < M; ++i)
+        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i].p[pa], b.p[pb], acc[i], 0, 0, 0);
+    }
+}
+
+// The operand that two neighbouring tiles of accumulators are: 8 consecutive
+// rows, of which the first tile has the upper four where g is odd.
+template <int IO>
+__device__ __forceinline__ Op<IO> tiles_op(f4 even, f4 odd, int g) {
+  const bool up = g & 1;
+  if constexpr (IO == 1) {
+    const u4 v = __builtin_bit_cast(u4, frag_regs<1>(even, odd).v);
+    const u4 w = {up ? v.z : v.x, up ? v.w : v.y, up ? v.x : v.z, up ? v.y : v.w};
+    return Op<1>{{__builtin_bit_cast(bf8, w)}};
+  } else {
+    float x[8];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      x[r] = up ? odd[r] : even[r];
+      x[4 + r] = up ? even[r] : odd[r];
+    }
+    return split<3>(x);
+  }
+}
 
 // The column (of a tile, or of the state) that row or column m of a wave's i-th
 // 16-wide product stands for. Two neighbouring i share 32 columns: m / 4 = c
@@ -172,13 +194,14 @@ struct Order {
 // All reads are (base ^ constant) + constant with a base that depends on the
 // lane alone: a step along the row changes bits that the exchange leaves to
 // the exclusive-or, and 4 or 32 rows further the exchange is the same.
+// A float32 tile lies there as its three parts, each a bfloat16 tile.
 template <int IO, int W, int NT>
 struct Tile {
   using T = typename Io<IO>::T;
-  static constexpr uint32_t kRow = W * sizeof(T);  // bytes
-  static constexpr uint32_t kBytes = kC * kRow;
-  static constexpr int kPer = kRow / 16;
-  static constexpr int kN = kC * kPer / NT;  // pieces of a thread
+  static constexpr int kParts = IO == 1 ? 1 : 3;
+  static constexpr uint32_t kRow = W * 2, kPart = kC * kRow, kBytes = kParts * kPart;  // bytes in LDS
+  static constexpr int kPer = W * sizeof(T) / 16;  // 16-byte pieces of a row in memory
+  static constexpr int kN = kC * kPer / NT;        // pieces of a thread
   u4 v[kN];
 
   static __device__ __forceinline__ uint32_t exchange(int row) {
@@ -186,10 +209,11 @@ struct Tile {
     // out; bit 2 is, for its rows are read apart; bits 1 and 3 must not meet
     // in bit 1, which tells the half pieces of one transposed read apart
     const int x = ((row >> 1) & 1) | ((row >> 3) & 2) | ((row >> 1) & 4);  // row bits 1, 4, 3
-    return kPer == 8 ? x : ((x & 1) << 2) | (x & 2) | ((x & 4) << 1) | (row & 1);
+    return W == 64 ? x : ((x & 1) << 2) | (x & 2) | ((x & 4) << 1) | (row & 1);
   }
-  static __device__ __forceinline__ uint32_t at(int row, int byte) {
-    return static_cast<uint32_t>(row) * kRow + (static_cast<uint32_t>(byte) ^ (exchange(row) << 4));
+  // Where element `col` of a row lies in each part.
+  static __device__ __forceinline__ uint32_t at(int row, int col) {
+    return static_cast<uint32_t>(row) * kRow + (static_cast<uint32_t>(2 * col) ^ (exchange(row) << 4));
   }
   // Rows 0 .. n - 1 of the chunk, row r at p + r * step (step in bytes, of either
   // sign); rows from n on and columns from `cols` on are zero: the buffer
@@ -214,48 +238,67 @@ struct Tile {
   }
   __device__ __forceinline__ void store(char* lds, uint32_t tid) const {
 #pragma unroll
-    for (int q = 0; q < kN; ++q)
-      *reinterpret_cast<u4*>(lds + at(tid / kPer + q * (NT / kPer), tid % kPer * 16)) = v[q];
+    for (int q = 0; q < kN; ++q) {
+      char* p = lds + at(tid / kPer + q * (NT / kPer), tid % kPer * (16 / sizeof(T)));
+      if constexpr (IO == 1) {
+        *reinterpret_cast<u4*>(p) = v[q];
+      } else {
+        put4(p, __builtin_bit_cast(f4, v[q]));
+      }
+    }
+  }
+  // Four neighbouring elements, rounded to bfloat16 or split into the parts.
+  static __device__ __forceinline__ void put4(char* p, f4 x) {
+    u2 o[kParts];
+    split4(x, o);
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) *reinterpret_cast<u2*>(p + i * kPart) = o[i];
+  }
+  static __device__ __forceinline__ f4 get4(const char* lds, int row, int col) {
+    f4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = kParts - 1; i >= 0; --i) {
+      const u2 o = *reinterpret_cast<const u2*>(lds + at(row, col) + i * kPart);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        x[2 * r] += __uint_as_float(o[r] << 16);
+        x[2 * r + 1] += __uint_as_float(o[r] & 0xFFFF0000u);
+      }
+    }
+    return x;
   }
 
   // Row-major operands, k-values 32 kb + 8 g .. of row spread(i, l15).
-  static __device__ __forceinline__ uint32_t row_base(int l15, int g) { return at(spread(0, l15), 8 * g * sizeof(T)); }
-  static __device__ __forceinline__ Frag<IO> row(const char* lds, uint32_t base, int i, int kb) {
-    const char* p = lds + 32 * (i >> 1) * kRow;
-    const uint32_t a = (base ^ (4 * (i & 1) * kRow)) ^ (32 * kb * sizeof(T));
-    if constexpr (IO == 1) {
-      return Frag<1>{__builtin_bit_cast(bf8, *reinterpret_cast<const u4*>(p + a))};
-    } else {
-      return Frag<0>{*reinterpret_cast<const f4*>(p + a), *reinterpret_cast<const f4*>(p + (a ^ 16))};
-    }
+  static __device__ __forceinline__ uint32_t row_base(int l15, int g) { return at(spread(0, l15), 8 * g); }
+  static __device__ __forceinline__ Op<IO> row(const char* lds, uint32_t base, int i, int kb) {
+    const char* p = lds + 32 * (i >> 1) * kRow + ((base ^ (4 * (i & 1) * kRow)) ^ (64 * kb));
+    Op<IO> f;
+#pragma unroll
+    for (int n = 0; n < kParts; ++n) f.p[n] = __builtin_bit_cast(bf8, *reinterpret_cast<const u4*>(p + n * kPart));
+    return f;
   }
   // Transposed operands: k runs over the tile's rows 32 kb + 8 g .., and lane
-  // l15 has column spread(i, l15).
+  // l15 has column spread(i, l15). A group of 16 lanes reads 4 columns of 4
+  // rows each and gets them transposed: lane l15 fetches row l15 / 4 of the
+  // columns of lanes 4 (l15 % 4) ..
   static __device__ __forceinline__ uint32_t col_base(int l15, int g) {
-    // bfloat16: a group of 16 lanes reads 4 columns of 4 rows each and gets
-    // them transposed: lane l15 fetches row l15 / 4 of the columns of lanes 4 (l15 % 4) ..
-    if constexpr (IO == 1) return at(8 * g + (l15 >> 2), spread(0, 4 * (l15 & 3)) * 2);
-    return at(8 * g, spread(0, l15) * 4);
+    return at(8 * g + (l15 >> 2), spread(0, 4 * (l15 & 3)));
   }
-  static __device__ __forceinline__ Frag<IO> col(const char* lds, uint32_t base, int i, int kb) {
-    const uint32_t a = base ^ (((i >> 1) * 32 + (i & 1) * 4) * sizeof(T));  // spread(i, .) is spread(0, .) ^ this
-    const char* p = lds + 32 * kb * kRow;
-    if constexpr (IO == 1) {
-      typedef short s4 __attribute__((ext_vector_type(4)));
-      typedef __attribute__((address_space(3))) s4* lds_s4;
-      const u2 lo = __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(p + a)));
-      const u2 hi = __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(p + 4 * kRow + a)));
-      const u4 v = {lo.x, lo.y, hi.x, hi.y};
-      return Frag<1>{__builtin_bit_cast(bf8, v)};
-    } else {
-      Frag<0> f;
+  // What takes a column base from spread(0, .) to spread(i, .).
+  static __device__ __forceinline__ uint32_t col_step(int i) { return (i >> 1) * 64 + (i & 1) * 8; }
+  static __device__ __forceinline__ Op<IO> col(const char* lds, uint32_t base, int i, int kb) {
+    typedef short s4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s4* lds_s4;
+    const char* p = lds + 32 * kb * kRow + (base ^ col_step(i));
+    Op<IO> f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        f.lo[j] = *reinterpret_cast<const float*>(p + j * kRow + (a ^ (exchange(j) << 4)));
-        f.hi[j] = *reinterpret_cast<const float*>(p + (4 + j) * kRow + (a ^ (exchange(4 + j) << 4)));
-      }
-      return f;
+    for (int n = 0; n < kParts; ++n) {
+      const u2 lo = __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(p + n * kPart)));
+      const u2 hi = __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(p + n * kPart + 4 * kRow)));
+      const u4 v = {lo.x, lo.y, hi.x, hi.y};
+      f.p[n] = __builtin_bit_cast(bf8, v);
     }
+    return f;
   }
 };
 
@@ -350,8 +393,13 @@ struct State {
   }
   // S^T = lam^n S^T + K^T (w V) over the tokens of the last document; w_in
   // holds the tokens' weights, keep is lam^n.
+  //
+  // The state is kept and returned in float32, so for bfloat16 io as well the
+  // products w v (24 significant bits) are three parts. Where the state is not
+  // returned, only y sees it, rounded to bfloat16 itself, and two parts (16
+  // bits) do; one would double the rounding that y gets.
   template <int IO, bool SEQ, typename TileK>
-  __device__ __forceinline__ void add(const char* Ks, uint32_t at_col, const Frag<IO> (&vf)[2], const float* w_in,
+  __device__ __forceinline__ void add(const char* Ks, uint32_t at_col, const Op<IO> (&vf)[2], const float* w_in,
                                       float keep, uint64_t begins, int g, bool three) {
     const int last = SEQ ? last_of(begins) : 0;
 #pragma unroll
@@ -360,46 +408,54 @@ struct State {
       for (int r = 0; r < 4; ++r) t[i][r] = SEQ && begins ? 0.0f : t[i][r] * keep;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
-      float x[8];
+      float x[8], bad = 0.0f;
       const f4 w[2] = {*reinterpret_cast<const f4*>(w_in + 32 * kb + 8 * g),
                        *reinterpret_cast<const f4*>(w_in + 32 * kb + 8 * g + 4)};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        x[j] = frag_get(vf[kb], j) * w[j >> 2][j & 3];
+        x[j] = get(vf[kb], j) * w[j >> 2][j & 3];
         if (SEQ) x[j] = 32 * kb + 8 * g + j >= last ? x[j] : 0.0f;
+        bad = fmaf(x[j], 0.0f, bad);
       }
-      Weighted<IO> wv;
-      wv.set(x, three);
+      Parts<3> wv = split<3>(x);
+      if (IO == 1 && __any(bad != 0.0f)) {  // an infinity or NaN is whole in its first part
+#pragma unroll
+        for (int p = 1; p < 3; ++p)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (!(x[j] - x[j] == 0.0f)) wv.p[p][j] = static_cast<__bf16>(0.0f);
+      }
       // four tiles at a time: their operands first, then one product with each part in turn
 #pragma unroll
       for (int i0 = 0; i0 < kTiles; i0 += 4) {
-        Frag<IO> kf[4];
+        Op<IO> kf[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           kf[i] = TileK::col(Ks, at_col, i0 + i, kb);
           // keys of other documents may hold infinities or NaN, which a weight of 0 would not remove
-          if (SEQ) kf[i] = frag_from(kf[i], last - (32 * kb + 8 * g));
+          if (SEQ) kf[i] = from_first(kf[i], last - (32 * kb + 8 * g));
         }
-#pragma unroll
-        for (int p = Weighted<IO>::kParts - 1; p >= 0; --p) {
-          if (p == 2 && !three) continue;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) t[i0 + i] = mma(kf[i], wv.part[p], t[i0 + i]);
-        }
+        if (IO == 0 || three)
+          mma_each(t + i0, kf, wv);
+        else
+          mma_each(t + i0, kf, Parts<2>{{wv.p[0], wv.p[1]}});
       }
     }
   }
 };
 
+// What lies in LDS: K, V and S twice each where they fit, then a chunk has one
+// barrier; else K and V twice and S once, or each once, with a second barrier
+// between the last reading of a chunk's and the writing of the next one's.
 template <int IO, int KD>
 struct Plan {
-  using T = typename Io<IO>::T;
   static constexpr int kThreadsY = 2 * kThreads;
   using TileK = Tile<IO, KD, kThreadsY>;
   using TileV = Tile<IO, kVS, kThreadsY>;
   using TileS = Tile<IO, KD, kThreadsY>;  // [column of v][k-element]
-  // the state once in LDS, with a second barrier, where twice would not fit
-  static constexpr int kSBuf = 2 * (TileK::kBytes + TileV::kBytes + TileS::kBytes) + 1024 <= 160 * 1024 ? 2 : 1;
+  static constexpr int kKV = TileK::kBytes + TileV::kBytes, kS = TileS::kBytes, kMost = 160 * 1024 - 1024;
+  static constexpr int kTBuf = 2 * kKV + kS <= kMost ? 2 : 1, kSBuf = 2 * kKV + 2 * kS <= kMost ? 2 : 1;
+  static_assert(kTBuf * kKV + kSBuf * kS <= kMost, "LDS");
 };
 
 template <int IO, int KD, bool SEQ>
@@ -410,8 +466,8 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
   using TileK = typename P::TileK;
   using TileV = typename P::TileV;
   using TileS = typename P::TileS;
-  constexpr int kKb = KD / 32, kSBuf = P::kSBuf;
-  constexpr uint32_t kBufK = 0, kBufV = 2 * TileK::kBytes, kBufS = kBufV + 2 * TileV::kBytes;
+  constexpr int kKb = KD / 32, kTBuf = P::kTBuf, kSBuf = P::kSBuf;
+  constexpr uint32_t kBufK = 0, kBufV = kTBuf * TileK::kBytes, kBufS = kBufV + kTBuf * TileV::kBytes;
   __shared__ __attribute__((aligned(512))) char lds[kBufS + kSBuf * TileS::kBytes];
   // powers of lam with their factors: of a score at distance 63 - m (0 from 64
   // on, above the diagonal), and of token s on its way into the state, for a
@@ -469,9 +525,9 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
     return begins;
   };
   auto put_tiles = [&](auto parity) {
-    constexpr int par = decltype(parity)::value;
-    kt[par].store(lds + kBufK + par * TileK::kBytes, tid);
-    vt[par].store(lds + kBufV + par * TileV::kBytes, tid);
+    constexpr int par = decltype(parity)::value, buf = par % kTBuf;
+    kt[par].store(lds + kBufK + buf * TileK::kBytes, tid);
+    vt[par].store(lds + kBufV + buf * TileV::kBytes, tid);
   };
   // The two tasks run loops of their own, so that neither holds the other's
   // registers; they meet at the same number of barriers.
@@ -497,17 +553,7 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
     // (rounded to bfloat16: the choice that makes y's products plain ones)
     auto put_state = [&](char* to) {
 #pragma unroll
-      for (int i = 0; i < State<KD>::kTiles; ++i) {
-        char* dst = to + TileS::at(spread(wv, l15), spread(i, 4 * g) * sizeof(T));
-        if constexpr (IO == 1) {
-          typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
-          const bf4 v = {static_cast<__bf16>(S.t[i][0]), static_cast<__bf16>(S.t[i][1]),
-                         static_cast<__bf16>(S.t[i][2]), static_cast<__bf16>(S.t[i][3])};
-          *reinterpret_cast<u2*>(dst) = __builtin_bit_cast(u2, v);
-        } else {
-          *reinterpret_cast<f4*>(dst) = S.t[i];
-        }
-      }
+      for (int i = 0; i < State<KD>::kTiles; ++i) TileS::put4(to + TileS::at(spread(wv, l15), spread(i, 4 * g)), S.t[i]);
     };
     start();
     S.zero();
@@ -527,7 +573,7 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
       w_in[wv][lane] = lane < n ? power(g2, n - off - lane) * sc_kv : 0.0f;
     }
     const uint32_t col_k = TileK::col_base(l15, g);
-    const uint32_t col_v = TileV::col_base(l15, g) ^ ((wv >> 1) * 32 + (wv & 1) * 4) * sizeof(T);
+    const uint32_t col_v = TileV::col_base(l15, g) ^ TileV::col_step(wv);
     all_chunks([&](int c, auto parity) {
       constexpr int par = decltype(parity)::value;
       const int n = min(kC, seqlen - c * kC);
@@ -536,11 +582,12 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
       int gg = g;
       asm volatile("" : "+v"(at_col), "+v"(at_v), "+v"(gg));
       if (c < c1) {
-        Frag<IO> vf[2];
+        Op<IO> vf[2];
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) vf[kb] = TileV::col(lds + kBufV + par * TileV::kBytes, at_v, 0, kb);
+        for (int kb = 0; kb < 2; ++kb) vf[kb] = TileV::col(lds + kBufV + par % kTBuf * TileV::kBytes, at_v, 0, kb);
         const float keep = n == kC ? keep_full : power(g2, n);
-        S.template add<IO, SEQ, TileK>(lds + kBufK + par * TileK::kBytes, at_col, vf, w_in[n < kC], keep, begins, gg, three);
+        S.template add<IO, SEQ, TileK>(lds + kBufK + par % kTBuf * TileK::kBytes, at_col, vf, w_in[n < kC], keep, begins, gg,
+                                       three);
       }
       if (kSBuf == 1) __syncthreads();  // the chunk's starting state has been read
       put_state(lds + kBufS + (kSBuf == 2 ? par ^ 1 : 0) * TileS::kBytes);
@@ -557,8 +604,9 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
   }
 
   // the wave's 16 tokens of q as operands; 0 beyond the sequence and beyond kd
-  Frag<IO> q[2][kKb];
-  auto fetch_q = [&](int c, Frag<IO> (&f)[kKb]) {
+  constexpr int kQ = sizeof(T) / 2;  // 16-byte pieces of 8 elements
+  u4 q[2][kKb][kQ];
+  auto fetch_q = [&](int c, u4 (&f)[kKb][kQ]) {
     const int n = c < c1 ? min(kC, seqlen - c * kC) : 0;
     const uint32_t stride = static_cast<uint32_t>(rev ? -qr.step : qr.step);
     const Order order(rev, n);
@@ -571,13 +619,9 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
     for (int kb = 0; kb < kKb; ++kb) {
       const int e = 32 * kb + 8 * g;
       const uint32_t o = in_range(at + e * sizeof(T), (t < n) & (e < kd));
-      const u4 x = __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, o, 0, 0));
-      if constexpr (IO == 1) {
-        f[kb] = Frag<1>{__builtin_bit_cast(bf8, x)};
-      } else {
-        const u4 y = __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, o + 16, 0, 0));
-        f[kb] = Frag<0>{__builtin_bit_cast(f4, x), __builtin_bit_cast(f4, y)};
-      }
+#pragma unroll
+      for (int i = 0; i < kQ; ++i)
+        f[kb][i] = __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, o + 16 * i, 0, 0));
     }
   };
   start();
@@ -589,8 +633,8 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
   all_chunks([&](int c, auto parity) {
     constexpr int par = decltype(parity)::value;
     const int n = c < c1 ? min(kC, seqlen - c * kC) : 0;
-    const char* const Ks = lds + kBufK + par * TileK::kBytes;
-    const char* const Vs = lds + kBufV + par * TileV::kBytes;
+    const char* const Ks = lds + kBufK + par % kTBuf * TileK::kBytes;
+    const char* const Vs = lds + kBufV + par % kTBuf * TileV::kBytes;
     const char* const Ss = lds + kBufS + (kSBuf == 2 ? par : 0) * TileS::kBytes;
     const uint64_t begins = begin(c, parity);
     uint32_t at_row = row_b, at_v = col_v;  // renewed: what follows from them is not kept over the loop
@@ -605,6 +649,16 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
     }
     f4 y[4];  // columns t, rows spread(i, 4 g) + r of the 64 columns of v
     if (c < c1) {
+      Op<IO> qf[kKb];
+#pragma unroll
+      for (int kb = 0; kb < kKb; ++kb) {
+        if constexpr (IO == 1) {
+          qf[kb] = Op<1>{{__builtin_bit_cast(bf8, q[par][kb][0])}};
+        } else {
+          const f4 lo = __builtin_bit_cast(f4, q[par][kb][0]), hi = __builtin_bit_cast(f4, q[par][kb][kQ - 1]);
+          qf[kb] = split<3>({lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w});
+        }
+      }
       // the scores: columns t, rows s; tiles 0 and 1 have s < 32, the other two are needed by the upper 32 tokens
       f4 sc[4];
 #pragma unroll
@@ -612,9 +666,10 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
         sc[2 * h] = sc[2 * h + 1] = f4{0.0f, 0.0f, 0.0f, 0.0f};
         if (h == 1 && wv < 2) break;
 #pragma unroll
-        for (int kb = 0; kb < kKb; ++kb)
-#pragma unroll
-          for (int i = 2 * h; i < 2 * h + 2; ++i) sc[i] = mma(TileK::row(Ks, at_row, i, kb), q[par][kb], sc[i]);
+        for (int kb = 0; kb < kKb; ++kb) {
+          const Op<IO> kf[2] = {TileK::row(Ks, at_row, 2 * h, kb), TileK::row(Ks, at_row, 2 * h + 1, kb)};
+          mma_each(sc + 2 * h, kf, qf[kb]);
+        }
 #pragma unroll
         for (int i = 2 * h; i < 2 * h + 2; ++i) {
           const int s = spread(i, 4 * gg);
@@ -629,9 +684,12 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int kb = 0; kb < kKb; ++kb)
+        for (int kb = 0; kb < kKb; ++kb) {
+          Op<IO> sf[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) y[i] = mma(TileS::row(Ss, at, i, kb), q[par][kb], y[i]);
+          for (int i = 0; i < 4; ++i) sf[i] = TileS::row(Ss, at, i, kb);
+          mma_each(y, sf, qf[kb]);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -639,13 +697,15 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
       };
       carried(at_row);
       // the scores are rounded to the io type here, once
-      const Frag<IO> s0 = state_frag<IO>(sc[0], sc[1], gg), s1 = state_frag<IO>(sc[2], sc[3], gg);
+      const Op<IO> s0 = tiles_op<IO>(sc[0], sc[1], gg), s1 = tiles_op<IO>(sc[2], sc[3], gg);
+      auto weighted = [&](const Op<IO>& p, int kb) {
+        Op<IO> vf[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = mma(TileV::col(Vs, at_v, i, 0), s0, y[i]);
-      if (wv >= 2) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = mma(TileV::col(Vs, at_v, i, 1), s1, y[i]);
-      }
+        for (int i = 0; i < 4; ++i) vf[i] = TileV::col(Vs, at_v, i, kb);
+        mma_each(y, vf, p);
+      };
+      weighted(s0, 0);
+      if (wv >= 2) weighted(s1, 1);
       float bad = 0.0f;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -663,13 +723,13 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             const int s = 32 * (k >> 3) + 8 * gs + (k & 7);
-            const float p = __shfl(k < 8 ? frag_get(s0, k & 7) : frag_get(s1, k & 7), 16 * gs + l15, 64);
+            const float p = __shfl(k < 8 ? get(s0, k & 7) : get(s1, k & 7), 16 * gs + l15, 64);
             if (s > t || s < from) continue;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const T* v = reinterpret_cast<const T*>(Vs + TileV::at(s, spread(i, 4 * gg) * sizeof(T)));
+              const f4 v = TileV::get4(Vs, s, spread(i, 4 * gg));
 #pragma unroll
-              for (int r = 0; r < 4; ++r) y[i][r] = fmaf(p, Io<IO>::load(v + r), y[i][r]);
+              for (int r = 0; r < 4; ++r) y[i][r] = fmaf(p, v[r], y[i][r]);
             }
           }
         }
@@ -696,8 +756,8 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, lo), rsrc, o, 0, 0);
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, hi), rsrc, o + 16, 0, 0);
       } else {
-        const Frag<1> v = state_frag<1>(y[2 * h], y[2 * h + 1], gg);
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, v.v), rsrc, o, 0, 0);
+        const Op<1> v = tiles_op<1>(y[2 * h], y[2 * h + 1], gg);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, v.p[0]), rsrc, o, 0, 0);
       }
     }
   });
@@ -706,13 +766,15 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
 // What each segment but the last adds to the state: the state's task alone,
 // four waves to a workgroup.
 template <int IO, int KD, bool SEQ>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 1 ? 3 : 1))) void la_sum_kernel(
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 1 ? 3 : 2))) void la_sum_kernel(
     const LaArgs a) {
   using T = typename Io<IO>::T;
   using TileK = Tile<IO, KD, kThreads>;
   using TileV = Tile<IO, kVS, kThreads>;
-  constexpr uint32_t kBufV = 2 * TileK::kBytes;
-  __shared__ __attribute__((aligned(512))) char lds[kBufV + 2 * TileV::kBytes];
+  // float32 tiles once, with a second barrier: two workgroups on a CU instead of one
+  constexpr int kTBuf = IO == 1 ? 2 : 1;
+  constexpr uint32_t kBufV = kTBuf * TileK::kBytes;
+  __shared__ __attribute__((aligned(512))) char lds[kBufV + kTBuf * TileV::kBytes];
   __shared__ float w_in[kC];
 
   const Place pl = place(a, a.nseg - 1);
@@ -753,20 +815,22 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 
   __syncthreads();
   auto chunk = [&](int c, auto parity) {
     constexpr int par = decltype(parity)::value;
-    const char* const Vs = lds + kBufV + par * TileV::kBytes;
+    const char* const Vs = lds + kBufV + par % kTBuf * TileV::kBytes;
     fetch(c + 2, kt[par], vt[par]);
     const uint64_t begins = SEQ && c < c1 ? ids[par].begins() : 0;
     seen |= begins != 0;
     if (SEQ) ids[par ^ 1].load(a.seq_idx, first, rev, c + 1, seqlen, lane);
     if (c < c1) {
-      const uint32_t at_v = TileV::col_base(l15, g) ^ ((wv >> 1) * 32 + (wv & 1) * 4) * sizeof(T);
-      Frag<IO> vf[2];
+      uint32_t at_col = TileK::col_base(l15, g), at_v = TileV::col_base(l15, g) ^ TileV::col_step(wv);
+      asm volatile("" : "+v"(at_col), "+v"(at_v));  // renewed, as in la_kernel
+      Op<IO> vf[2];
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) vf[kb] = TileV::col(Vs, at_v, 0, kb);
-      S.template add<IO, SEQ, TileK>(lds + par * TileK::kBytes, TileK::col_base(l15, g), vf, w_in, keep, begins, g, three);
+      S.template add<IO, SEQ, TileK>(lds + par % kTBuf * TileK::kBytes, at_col, vf, w_in, keep, begins, g, three);
     }
-    kt[par ^ 1].store(lds + (par ^ 1) * TileK::kBytes, tid);
-    vt[par ^ 1].store(lds + kBufV + (par ^ 1) * TileV::kBytes, tid);
+    if (kTBuf == 1) __syncthreads();
+    kt[par ^ 1].store(lds + (par ^ 1) % kTBuf * TileK::kBytes, tid);
+    vt[par ^ 1].store(lds + kBufV + (par ^ 1) % kTBuf * TileV::kBytes, tid);
     __syncthreads();
   };
   for (int c = c0; c < c1; c += 2) {  // the second of the last two may be empty
