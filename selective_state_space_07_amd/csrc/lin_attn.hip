@@ -26,7 +26,9 @@
 // the last; each chunk's starting state goes to the first four through LDS.
 // Both tasks of a chunk run at once, one wave of each on a SIMD, and with K, V
 // and S in LDS twice there is one barrier to a chunk. K and V come through
-// registers two chunks ahead, Q straight into the lanes that multiply it.
+// registers two chunks ahead (one where the registers do not suffice), Q
+// straight into the lanes that multiply it. A chunk is bound by the issue of
+// its instructions, so places in memory are worked out once for all chunks.
 //
 // float32 io runs on the bfloat16 matrix cores as well, sixteen times as fast
 // as the float32 ones: every operand is the sum of three bfloat16 parts of 8
@@ -176,11 +178,33 @@ __device__ __forceinline__ int spread(int i, int m) {
 __device__ __forceinline__ uint32_t in_range(uint32_t off, bool ok) {
   return off | ((static_cast<uint32_t>(ok) - 1u) & 0xFFFFFFC0u);
 }
-// The place of row r in memory of n rows that lie upwards, or downwards.
+// The rows of a chunk lie upwards in memory, or downwards where the sum runs
+// from the last token to the first. `low` is the row that lies lowest; row r of
+// a whole chunk is at far(r) * stride from it, and in a last chunk of n rows
+// that runs downwards all of them are cut(n) * stride nearer. Rows from n on
+// are then out of the range of the buffer, above it or (as unsigned numbers)
+// below 0: strides are at most 2^26 bytes.
 struct Order {
-  int base, sign;
-  __device__ __forceinline__ Order(bool rev, int n) : base(rev ? n - 1 : 0), sign(rev ? -1 : 1) {}
-  __device__ __forceinline__ uint32_t operator()(int r) const { return static_cast<uint32_t>(base + sign * r); }
+  bool rev;
+  __device__ __forceinline__ uint32_t far(int r) const { return static_cast<uint32_t>(rev ? kC - 1 - r : r); }
+  __device__ __forceinline__ uint32_t cut(int n) const { return static_cast<uint32_t>(rev ? kC - n : 0); }
+  __device__ __forceinline__ int64_t low(int n) const { return rev ? n - 1 : 0; }  // in rows from the first
+};
+// A matrix of which a workgroup walks the chunks: the first token's row, the
+// bytes from a row to the next one in memory, and those of a row that are read.
+struct Rows {
+  const char* p;
+  uint32_t stride, width;
+  Order order;
+  // n rows from chunk c on; none are in range where n <= 0. No branch may stand
+  // around a load: behind one the compiler could not tell the loads in flight
+  // apart and would wait for all of them.
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk(int c, int n) const {
+    const int64_t row = static_cast<int64_t>(c) * kC + order.low(n);
+    const char* at = p + (order.rev ? -row : row) * stride;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(at), 0,
+                                             n > 0 ? stride * static_cast<uint32_t>(n - 1) + width : 0, 0x00020000);
+  }
 };
 
 // A 64-row tile of W columns in LDS and its way there from global memory
@@ -215,26 +239,24 @@ struct Tile {
   static __device__ __forceinline__ uint32_t at(int row, int col) {
     return static_cast<uint32_t>(row) * kRow + (static_cast<uint32_t>(2 * col) ^ (exchange(row) << 4));
   }
-  // Rows 0 .. n - 1 of the chunk, row r at p + r * step (step in bytes, of either
-  // sign); rows from n on and columns from `cols` on are zero: the buffer
-  // range's answer to an offset out of range. With n <= 0 nothing is read, and
-  // no branch stands around a load: behind one the compiler could not tell the
-  // loads in flight apart and would wait for all of them.
-  __device__ __forceinline__ void load(const void* p, int64_t step, int n, int cols, uint32_t tid) {
-    const uint32_t stride = static_cast<uint32_t>(step < 0 ? -step : step), width = min(cols, W) * sizeof(T);
-    const Order order(step < 0, n);
-    const char* low = static_cast<const char*>(p) + step * order.base;
-    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<char*>(low), 0, n > 0 ? stride * static_cast<uint32_t>(n - 1) + width : 0, 0x00020000);
-    // a thread's pieces lie in one column, NT / kPer rows apart
-    asm volatile("" : "+v"(tid));  // the offsets are cheaper made again than kept over the loop
-    const uint32_t c = tid % kPer * 16;
+  // The places of a thread's pieces in a whole chunk; those of columns that
+  // are not read are out of every range.
+  struct Ways {
+    uint32_t at[kN];
+    __device__ __forceinline__ Ways(const Rows& m, uint32_t tid) {
+      const uint32_t c = tid % kPer * 16;  // one column, NT / kPer rows apart
 #pragma unroll
-    for (int q = 0; q < kN; ++q) {
-      const int r = static_cast<int>(tid / kPer) + q * (NT / kPer);
-      const uint32_t off = in_range(order(r) * stride + c, (r < n) & (c < width));
-      v[q] = __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, off, 0, 0));
+      for (int q = 0; q < kN; ++q)
+        at[q] = in_range(m.order.far(static_cast<int>(tid / kPer) + q * (NT / kPer)) * m.stride + c, c < m.width);
     }
+  };
+  // n rows of a chunk; 0 behind them and beyond the columns
+  __device__ __forceinline__ void load(const Rows& m, const Ways& w, int c, int n) {
+    const auto rsrc = m.chunk(c, n);
+    const uint32_t cut = m.order.cut(n) * m.stride;
+#pragma unroll
+    for (int q = 0; q < kN; ++q)
+      v[q] = __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, w.at[q] - cut, 0, 0));
   }
   __device__ __forceinline__ void store(char* lds, uint32_t tid) const {
 #pragma unroll
@@ -334,18 +356,13 @@ __device__ __forceinline__ int64_t ws_base(const LaArgs& a, const Place& p, int 
 
 // What a workgroup reads: the rows of one operand and head, from the first
 // token on in the direction of the sum.
-struct Rows {
-  const char* p;
-  int64_t step;  // bytes from a token to the next one
-};
 template <typename T>
-__device__ __forceinline__ Rows rows_of(const LaOperand& o, const Place& pl, int rep, int width, int64_t first, bool rev) {
-  const int64_t head = static_cast<int64_t>(o.per_group ? pl.h / rep : pl.h) * width;
-  const int64_t step = o.row * static_cast<int64_t>(sizeof(T));
-  return Rows{reinterpret_cast<const char*>(static_cast<const T*>(o.p) + first * o.row + head), rev ? -step : step};
-}
-__device__ __forceinline__ const char* chunk_of(const Rows& r, int c) {
-  return r.p + static_cast<int64_t>(c) * kC * r.step;
+__device__ __forceinline__ Rows rows_of(const LaOperand& o, const Place& pl, int rep, int width, int from, int most,
+                                        int64_t first, bool rev) {
+  const int64_t head = static_cast<int64_t>(o.per_group ? pl.h / rep : pl.h) * width + from;
+  return Rows{reinterpret_cast<const char*>(static_cast<const T*>(o.p) + first * o.row + head),
+              static_cast<uint32_t>(o.row * static_cast<int64_t>(sizeof(T))),
+              static_cast<uint32_t>(min(width - from, most) * sizeof(T)), Order{rev}};
 }
 
 // The first tokens of documents among a chunk's 64, as bits (each wave asks
@@ -358,9 +375,8 @@ struct Ids {
     const int32_t* low = seq_idx + first + (rev ? -static_cast<int64_t>(c * kC + kC - 1) : c * kC - 1);
     const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<int32_t*>(low), 0, (kC + 1) * 4, 0x00020000);
     const bool ok = (pos < seqlen) & (pos > 0);
-    const Order order(rev, kC + 1);
-    own = __builtin_amdgcn_raw_buffer_load_b32(rsrc, in_range(4 * order(lane + 1), ok), 0, 0);
-    prev = __builtin_amdgcn_raw_buffer_load_b32(rsrc, in_range(4 * order(lane), ok), 0, 0);
+    own = __builtin_amdgcn_raw_buffer_load_b32(rsrc, in_range(4 * (rev ? kC - 1 - lane : lane + 1), ok), 0, 0);
+    prev = __builtin_amdgcn_raw_buffer_load_b32(rsrc, in_range(4 * (rev ? kC - lane : lane), ok), 0, 0);
   }
   __device__ __forceinline__ uint64_t begins() const { return __ballot(own != prev); }
 };
@@ -430,10 +446,11 @@ struct State {
       for (int i0 = 0; i0 < kTiles; i0 += 4) {
         Op<IO> kf[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          kf[i] = TileK::col(Ks, at_col, i0 + i, kb);
-          // keys of other documents may hold infinities or NaN, which a weight of 0 would not remove
-          if (SEQ) kf[i] = from_first(kf[i], last - (32 * kb + 8 * g));
+        for (int i = 0; i < 4; ++i) kf[i] = TileK::col(Ks, at_col, i0 + i, kb);
+        // keys of other documents may hold infinities or NaN, which a weight of 0 would not remove
+        if (SEQ && begins) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) kf[i] = from_first(kf[i], last - (32 * kb + 8 * g));
         }
         if (IO == 0 || three)
           mma_each(t + i0, kf, wv);
@@ -456,6 +473,8 @@ struct Plan {
   static constexpr int kKV = TileK::kBytes + TileV::kBytes, kS = TileS::kBytes, kMost = 160 * 1024 - 1024;
   static constexpr int kTBuf = 2 * kKV + kS <= kMost ? 2 : 1, kSBuf = 2 * kKV + 2 * kS <= kMost ? 2 : 1;
   static_assert(kTBuf * kKV + kSBuf * kS <= kMost, "LDS");
+  // chunks that K, V and Q are ahead in registers: two, or one where two do not fit
+  static constexpr int kAhead = IO == 0 && KD == 128 ? 1 : 2;
 };
 
 template <int IO, int KD, bool SEQ>
@@ -466,7 +485,7 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
   using TileK = typename P::TileK;
   using TileV = typename P::TileV;
   using TileS = typename P::TileS;
-  constexpr int kKb = KD / 32, kTBuf = P::kTBuf, kSBuf = P::kSBuf;
+  constexpr int kKb = KD / 32, kTBuf = P::kTBuf, kSBuf = P::kSBuf, kAhead = P::kAhead;
   constexpr uint32_t kBufK = 0, kBufV = kTBuf * TileK::kBytes, kBufS = kBufV + kTBuf * TileV::kBytes;
   __shared__ __attribute__((aligned(512))) char lds[kBufS + kSBuf * TileS::kBytes];
   // powers of lam with their factors: of a score at distance 63 - m (0 from 64
@@ -496,38 +515,39 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
   const int c0 = pl.seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, nchunks);
   const float g2 = a.log_decay[pl.h] * kLog2e;
   const int64_t first = static_cast<int64_t>(pl.b) * seqlen + (rev ? seqlen - 1 : 0);
-  const Rows qr = rows_of<T>(R.q, pl, rep, kd, first, rev), kr = rows_of<T>(R.k, pl, rep, kd, first, rev);
-  Rows vr = rows_of<T>(R.v, pl, rep, vd, first, rev);
-  vr.p += v0 * sizeof(T);
+  const Rows qr = rows_of<T>(R.q, pl, rep, kd, 0, KD, first, rev), kr = rows_of<T>(R.k, pl, rep, kd, 0, KD, first, rev);
+  const Rows vr = rows_of<T>(R.v, pl, rep, vd, v0, kVS, first, rev);
 
   const float keep_full = power(g2, kC);
 
-  TileK kt[2];
-  TileV vt[2];
+  TileK kt[kAhead];
+  TileV vt[kAhead];
   Ids ids[2];
+  const typename TileK::Ways way_k(kr, tid);
+  const typename TileV::Ways way_v(vr, tid);
   auto fetch = [&](int c, TileK& k, TileV& v) {
     const int n = c < c1 ? min(kC, seqlen - c * kC) : 0;
-    k.load(chunk_of(kr, c), kr.step, n, kd, tid);
-    v.load(chunk_of(vr, c), vr.step, n, vd - v0, tid);
+    k.load(kr, way_k, c, n);
+    v.load(vr, way_v, c, n);
   };
   auto start = [&]() {
     fetch(c0, kt[0], vt[0]);
-    fetch(c0 + 1, kt[1], vt[1]);
+    if (kAhead == 2) fetch(c0 + 1, kt[kAhead - 1], vt[kAhead - 1]);
     if (SEQ) ids[0].load(a.seq_idx, first, rev, c0, seqlen, lane);
   };
   // A chunk's beginning, for either task: the tiles two chunks on start their
   // way, and the wave learns where documents begin.
   auto begin = [&](int c, auto parity) {
     constexpr int par = decltype(parity)::value;
-    fetch(c + 2, kt[par], vt[par]);
+    fetch(c + kAhead, kt[par % kAhead], vt[par % kAhead]);
     const uint64_t begins = SEQ ? ids[par].begins() : 0;
     if (SEQ) ids[par ^ 1].load(a.seq_idx, first, rev, c + 1, seqlen, lane);
     return begins;
   };
   auto put_tiles = [&](auto parity) {
     constexpr int par = decltype(parity)::value, buf = par % kTBuf;
-    kt[par].store(lds + kBufK + buf * TileK::kBytes, tid);
-    vt[par].store(lds + kBufV + buf * TileV::kBytes, tid);
+    kt[par % kAhead].store(lds + kBufK + buf * TileK::kBytes, tid);
+    vt[par % kAhead].store(lds + kBufV + buf * TileV::kBytes, tid);
   };
   // The two tasks run loops of their own, so that neither holds the other's
   // registers; they meet at the same number of barriers.
@@ -586,8 +606,8 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) vf[kb] = TileV::col(lds + kBufV + par % kTBuf * TileV::kBytes, at_v, 0, kb);
         const float keep = n == kC ? keep_full : power(g2, n);
-        S.template add<IO, SEQ, TileK>(lds + kBufK + par % kTBuf * TileK::kBytes, at_col, vf, w_in[n < kC], keep, begins, gg,
-                                       three);
+        const char* Ks = lds + kBufK + par % kTBuf * TileK::kBytes;
+        S.template add<IO, SEQ, TileK>(Ks, at_col, vf, w_in[n < kC], keep, begins, gg, three);
       }
       if (kSBuf == 1) __syncthreads();  // the chunk's starting state has been read
       put_state(lds + kBufS + (kSBuf == 2 ? par ^ 1 : 0) * TileS::kBytes);
@@ -605,30 +625,33 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
 
   // the wave's 16 tokens of q as operands; 0 beyond the sequence and beyond kd
   constexpr int kQ = sizeof(T) / 2;  // 16-byte pieces of 8 elements
-  u4 q[2][kKb][kQ];
+  u4 q[kAhead][kKb][kQ];
+  uint32_t way_q[kKb];
+#pragma unroll
+  for (int kb = 0; kb < kKb; ++kb)
+    way_q[kb] = in_range(qr.order.far(16 * wv + l15) * qr.stride + (32 * kb + 8 * g) * sizeof(T), 32 * kb + 8 * g < kd);
   auto fetch_q = [&](int c, u4 (&f)[kKb][kQ]) {
     const int n = c < c1 ? min(kC, seqlen - c * kC) : 0;
-    const uint32_t stride = static_cast<uint32_t>(rev ? -qr.step : qr.step);
-    const Order order(rev, n);
-    const char* low = chunk_of(qr, c) + qr.step * order.base;
-    const uint32_t bytes = n > 0 ? stride * static_cast<uint32_t>(n - 1) + kd * static_cast<uint32_t>(sizeof(T)) : 0;
-    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(low), 0, bytes, 0x00020000);
-    const int t = 16 * wv + l15;
-    const uint32_t at = order(t) * stride;
+    const auto rsrc = qr.chunk(c, n);
+    const uint32_t cut = qr.order.cut(n) * qr.stride;
 #pragma unroll
-    for (int kb = 0; kb < kKb; ++kb) {
-      const int e = 32 * kb + 8 * g;
-      const uint32_t o = in_range(at + e * sizeof(T), (t < n) & (e < kd));
+    for (int kb = 0; kb < kKb; ++kb)
 #pragma unroll
       for (int i = 0; i < kQ; ++i)
-        f[kb][i] = __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, o + 16 * i, 0, 0));
-    }
+        f[kb][i] = __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, way_q[kb] - cut, 16 * i, 0));
   };
   start();
   fetch_q(c0, q[0]);
-  fetch_q(c0 + 1, q[1]);
+  if (kAhead == 2) fetch_q(c0 + 1, q[kAhead - 1]);
   if (tid < 96) w_score[tid] = tid < kC ? power(g2, 63 - tid) * (sc_out * sc_kv) : 0.0f;
   const float w_out = power(g2, 16 * wv + l15 + off) * sc_out;  // of the state read at this lane's token
+  const int64_t out_row = static_cast<int64_t>(nheads) * vd;
+  const Rows outs{static_cast<char*>(out_p) + (first * out_row + static_cast<int64_t>(pl.h) * vd + v0) * es_out,
+                  static_cast<uint32_t>(out_row * es_out), static_cast<uint32_t>(min(vd - v0, kVS) * es_out), Order{rev}};
+  uint32_t way_out[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    way_out[h] = in_range(outs.order.far(16 * wv + l15) * outs.stride + (32 * h + 8 * g) * es_out, 32 * h + 8 * g < vd - v0);
   const uint32_t row_b = TileK::row_base(l15, g), col_v = TileV::col_base(l15, g);
   all_chunks([&](int c, auto parity) {
     constexpr int par = decltype(parity)::value;
@@ -647,18 +670,19 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
       from = last_of(m);
       open = m == 0;
     }
+    Op<IO> qf[kKb];
+#pragma unroll
+    for (int kb = 0; kb < kKb; ++kb) {
+      if constexpr (IO == 1) {
+        qf[kb] = Op<1>{{__builtin_bit_cast(bf8, q[par % kAhead][kb][0])}};
+      } else {
+        const f4 lo = __builtin_bit_cast(f4, q[par % kAhead][kb][0]), hi = __builtin_bit_cast(f4, q[par % kAhead][kb][kQ - 1]);
+        qf[kb] = split<3>({lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w});
+      }
+    }
+    if (kAhead == 1) fetch_q(c + 1, q[0]);  // what it held is in the parts
     f4 y[4];  // columns t, rows spread(i, 4 g) + r of the 64 columns of v
     if (c < c1) {
-      Op<IO> qf[kKb];
-#pragma unroll
-      for (int kb = 0; kb < kKb; ++kb) {
-        if constexpr (IO == 1) {
-          qf[kb] = Op<1>{{__builtin_bit_cast(bf8, q[par][kb][0])}};
-        } else {
-          const f4 lo = __builtin_bit_cast(f4, q[par][kb][0]), hi = __builtin_bit_cast(f4, q[par][kb][kQ - 1]);
-          qf[kb] = split<3>({lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w});
-        }
-      }
       // the scores: columns t, rows s; tiles 0 and 1 have s < 32, the other two are needed by the upper 32 tokens
       f4 sc[4];
 #pragma unroll
@@ -676,8 +700,8 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
           const float* w = w_score + 63 - t + s;
           const f4 wt = {w[0], w[1], w[2], w[3]};
 #pragma unroll
-          for (int r = 0; r < 4; ++r)  // chosen, not multiplied, so that masked pairs drop infinities and NaN
-            sc[i][r] = ((s + r <= t) & (s + r >= from)) ? sc[i][r] * wt[r] : 0.0f;
+          for (int r = 0; r < 4; ++r)  // later tokens have weight 0, those of other documents are dropped
+            sc[i][r] = !SEQ || s + r >= from ? sc[i][r] * wt[r] : 0.0f;
         }
       }
       auto carried = [&](uint32_t at) {
@@ -711,9 +735,9 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r) bad = fmaf(y[i][r], 0.0f, bad);
-      // An infinity or NaN in v also reaches the tokens that it is masked for,
-      // as 0 * inf. Where any sum is not finite the sums are taken again, over
-      // the unmasked tokens alone.
+      // An infinity or NaN in k or v also reaches the tokens that it is masked
+      // for, as 0 * inf. Where any sum is not finite the sums are taken again,
+      // over the unmasked tokens alone.
       if (__any(bad != 0.0f)) {
         uint32_t again = at_row;
         asm volatile("" : "+v"(again));  // read again, not kept from above
@@ -736,20 +760,15 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
       }
     }
     if (kSBuf == 1) __syncthreads();  // the chunk's starting state has been read
-    fetch_q(c + 2, q[par]);
+    if (kAhead == 2) fetch_q(c + 2, q[par % kAhead]);
     // Two tiles are 8 neighbouring columns of a token, the upper four first
     // where g is odd. Rows from n on and columns from vd on are out of the
     // buffer's range and dropped.
-    const uint32_t row_out = static_cast<uint32_t>(nheads) * vd * es_out;
-    const Order order(rev, n);
-    const int64_t low = first + (rev ? -1 : 1) * static_cast<int64_t>(c * kC + order.base);
-    char* const out = static_cast<char*>(out_p) + ((low * nheads + pl.h) * vd + v0) * es_out;
-    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(out, 0, n > 0 ? row_out * (n - 1) + (vd - v0) * es_out : 0, 0x00020000);
-    const uint32_t o_row = order(t) * row_out;
+    const auto rsrc = outs.chunk(c, n);
+    const uint32_t cut = outs.order.cut(n) * outs.stride;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int oc = 32 * h + 8 * gg;
-      const uint32_t o = in_range(o_row + oc * es_out, (t < n) & (oc < vd - v0));
+      const uint32_t o = way_out[h] - cut;
       if (IO == 0 || es_out == 4) {
         const bool up = gg & 1;
         const f4 lo = up ? y[2 * h + 1] : y[2 * h], hi = up ? y[2 * h] : y[2 * h + 1];
@@ -772,7 +791,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 
   using TileK = Tile<IO, KD, kThreads>;
   using TileV = Tile<IO, kVS, kThreads>;
   // float32 tiles once, with a second barrier: two workgroups on a CU instead of one
-  constexpr int kTBuf = IO == 1 ? 2 : 1;
+  constexpr int kTBuf = IO == 1 ? 2 : 1, kAhead = IO == 0 && KD == 128 ? 1 : 2;
   constexpr uint32_t kBufV = kTBuf * TileK::kBytes;
   __shared__ __attribute__((aligned(512))) char lds[kBufV + kTBuf * TileV::kBytes];
   __shared__ float w_in[kC];
@@ -789,21 +808,22 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 
   const int c0 = pl.seg * a.seg_chunks, c1 = c0 + a.seg_chunks;  // whole chunks: a later segment follows
   const float g2 = a.log_decay[pl.h] * kLog2e;
   const int64_t first = static_cast<int64_t>(pl.b) * seqlen + (rev ? seqlen - 1 : 0);
-  const Rows kr = rows_of<T>(R.k, pl, rep, kd, first, rev);
-  Rows vr = rows_of<T>(R.v, pl, rep, vd, first, rev);
-  vr.p += v0 * sizeof(T);
+  const Rows kr = rows_of<T>(R.k, pl, rep, kd, 0, KD, first, rev);
+  const Rows vr = rows_of<T>(R.v, pl, rep, vd, v0, kVS, first, rev);
   const bool three = __builtin_amdgcn_readfirstlane(R.state_out != nullptr) != 0;
 
-  TileK kt[2];
-  TileV vt[2];
+  TileK kt[kAhead];
+  TileV vt[kAhead];
   Ids ids[2];
+  const typename TileK::Ways way_k(kr, tid);
+  const typename TileV::Ways way_v(vr, tid);
   auto fetch = [&](int c, TileK& k, TileV& v) {
     const int n = c < c1 ? kC : 0;
-    k.load(chunk_of(kr, c), kr.step, n, kd, tid);
-    v.load(chunk_of(vr, c), vr.step, n, vd - v0, tid);
+    k.load(kr, way_k, c, n);
+    v.load(vr, way_v, c, n);
   };
   fetch(c0, kt[0], vt[0]);
-  fetch(c0 + 1, kt[1], vt[1]);
+  if (kAhead == 2) fetch(c0 + 1, kt[kAhead - 1], vt[kAhead - 1]);
   if (SEQ) ids[0].load(a.seq_idx, first, rev, c0, seqlen, lane);
   if (tid < kC) w_in[tid] = power(g2, kC - R.off - tid) * R.sc_kv;
   const float keep = power(g2, kC);
@@ -816,7 +836,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 
   auto chunk = [&](int c, auto parity) {
     constexpr int par = decltype(parity)::value;
     const char* const Vs = lds + kBufV + par % kTBuf * TileV::kBytes;
-    fetch(c + 2, kt[par], vt[par]);
+    fetch(c + kAhead, kt[par % kAhead], vt[par % kAhead]);
     const uint64_t begins = SEQ && c < c1 ? ids[par].begins() : 0;
     seen |= begins != 0;
     if (SEQ) ids[par ^ 1].load(a.seq_idx, first, rev, c + 1, seqlen, lane);
@@ -826,11 +846,12 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 
       Op<IO> vf[2];
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) vf[kb] = TileV::col(Vs, at_v, 0, kb);
-      S.template add<IO, SEQ, TileK>(lds + par % kTBuf * TileK::kBytes, at_col, vf, w_in, keep, begins, g, three);
+      const char* Ks = lds + par % kTBuf * TileK::kBytes;
+      S.template add<IO, SEQ, TileK>(Ks, at_col, vf, w_in, keep, begins, g, three);
     }
     if (kTBuf == 1) __syncthreads();
-    kt[par ^ 1].store(lds + (par ^ 1) % kTBuf * TileK::kBytes, tid);
-    vt[par ^ 1].store(lds + kBufV + (par ^ 1) % kTBuf * TileV::kBytes, tid);
+    kt[(par ^ 1) % kAhead].store(lds + (par ^ 1) % kTBuf * TileK::kBytes, tid);
+    vt[(par ^ 1) % kAhead].store(lds + kBufV + (par ^ 1) % kTBuf * TileV::kBytes, tid);
     __syncthreads();
   };
   for (int c = c0; c < c1; c += 2) {  // the second of the last two may be empty
