@@ -72,37 +72,35 @@ struct Parts {
 template <int IO>
 using Op = Parts<IO == 1 ? 1 : 3>;
 
-// Each part is the rounded rest of those before it.
+// Two values as one word of bfloat16, which is taken off them: each part of a
+// value is the rounded rest of those before it.
+__device__ __forceinline__ uint32_t take(float& a, float& b) {
+  typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+  const uint32_t w = __builtin_bit_cast(uint32_t, bf2{static_cast<__bf16>(a), static_cast<__bf16>(b)});
+  a -= __uint_as_float(w << 16);
+  b -= __uint_as_float(w & 0xFFFF0000u);
+  return w;
+}
+__device__ __forceinline__ bf8 take(float (&x)[8]) {
+  u4 w;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = take(x[2 * j], x[2 * j + 1]);
+  return __builtin_bit_cast(bf8, w);
+}
 template <int N>
-__device__ __forceinline__ Parts<N> split(const float (&x)[8]) {
+__device__ __forceinline__ Parts<N> split(f4 lo, f4 hi) {
+  float x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
   Parts<N> o;
-  float r[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) r[j] = x[j];
-#pragma unroll
-  for (int p = 0; p < N; ++p)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const __bf16 h = static_cast<__bf16>(r[j]);
-      o.p[p][j] = h;
-      if (p + 1 < N) r[j] -= static_cast<float>(h);
-    }
+  for (int p = 0; p < N; ++p) o.p[p] = take(x);
   return o;
 }
 // The same of four values, two to a word.
 template <int N>
-__device__ __forceinline__ void split4(f4 x, u2 (&o)[N]) {
-  typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ void split4(f4 v, u2 (&o)[N]) {
+  float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int p = 0; p < N; ++p) {
-    const bf4 h = {static_cast<__bf16>(x[0]), static_cast<__bf16>(x[1]), static_cast<__bf16>(x[2]),
-                   static_cast<__bf16>(x[3])};
-    o[p] = __builtin_bit_cast(u2, h);
-    if (p + 1 < N) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) x[r] -= static_cast<float>(h[r]);
-    }
-  }
+  for (int p = 0; p < N; ++p) o[p] = u2{take(x[0], x[1]), take(x[2], x[3])};
 }
 // Element j as float32.
 template <int N>
@@ -153,13 +151,7 @@ __device__ __forceinline__ Op<IO> tiles_op(f4 even, f4 odd, int g) {
     const u4 w = {up ? v.z : v.x, up ? v.w : v.y, up ? v.x : v.z, up ? v.y : v.w};
     return Op<1>{{__builtin_bit_cast(bf8, w)}};
   } else {
-    float x[8];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      x[r] = up ? odd[r] : even[r];
-      x[4 + r] = up ? even[r] : odd[r];
-    }
-    return split<3>(x);
+    return split<3>(up ? odd : even, up ? even : odd);
   }
 }
 
@@ -433,30 +425,34 @@ struct State {
         if (SEQ) x[j] = 32 * kb + 8 * g + j >= last ? x[j] : 0.0f;
         bad = fmaf(x[j], 0.0f, bad);
       }
-      Parts<3> wv = split<3>(x);
-      if (IO == 1 && __any(bad != 0.0f)) {  // an infinity or NaN is whole in its first part
-#pragma unroll
-        for (int p = 1; p < 3; ++p)
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (!(x[j] - x[j] == 0.0f)) wv.p[p][j] = static_cast<__bf16>(0.0f);
-      }
+      bf8 wv[2] = {take(x), take(x)};
       // four tiles at a time: their operands first, then one product with each part in turn
+      auto products = [&](const auto& parts) {
 #pragma unroll
-      for (int i0 = 0; i0 < kTiles; i0 += 4) {
-        Op<IO> kf[4];
+        for (int i0 = 0; i0 < kTiles; i0 += 4) {
+          Op<IO> kf[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) kf[i] = TileK::col(Ks, at_col, i0 + i, kb);
-        // keys of other documents may hold infinities or NaN, which a weight of 0 would not remove
-        if (SEQ && begins) {
+          for (int i = 0; i < 4; ++i) kf[i] = TileK::col(Ks, at_col, i0 + i, kb);
+          // keys of other documents may hold infinities or NaN, which a weight of 0 would not remove
+          if (SEQ && begins) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) kf[i] = from_first(kf[i], last - (32 * kb + 8 * g));
+            for (int i = 0; i < 4; ++i) kf[i] = from_first(kf[i], last - (32 * kb + 8 * g));
+          }
+          mma_each(t + i0, kf, parts);
         }
-        if (IO == 0 || three)
-          mma_each(t + i0, kf, wv);
-        else
-          mma_each(t + i0, kf, Parts<2>{{wv.p[0], wv.p[1]}});
+      };
+      if (IO == 1 && __any(bad != 0.0f)) {  // an infinity or NaN is whole in its first part, and its rest is NaN
+        asm volatile("");                   // a branch, not selects
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          x[j] = x[j] == x[j] ? x[j] : 0.0f;
+          if (!(static_cast<float>(wv[1][j]) == static_cast<float>(wv[1][j]))) wv[1][j] = static_cast<__bf16>(0.0f);
+        }
       }
+      if (IO == 0 || three)
+        products(Parts<3>{{wv[0], wv[1], take(x)}});
+      else
+        products(Parts<2>{{wv[0], wv[1]}});
     }
   }
 };
@@ -677,7 +673,7 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
         qf[kb] = Op<1>{{__builtin_bit_cast(bf8, q[par % kAhead][kb][0])}};
       } else {
         const f4 lo = __builtin_bit_cast(f4, q[par % kAhead][kb][0]), hi = __builtin_bit_cast(f4, q[par % kAhead][kb][kQ - 1]);
-        qf[kb] = split<3>({lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w});
+        qf[kb] = split<3>(lo, hi);
       }
     }
     if (kAhead == 1) fetch_q(c + 1, q[0]);  // what it held is in the parts
@@ -783,17 +779,16 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
 }
 
 // What each segment but the last adds to the state: the state's task alone,
-// four waves to a workgroup.
+// four waves to a workgroup and two or three workgroups to a CU, so that one
+// chunk ahead suffices.
 template <int IO, int KD, bool SEQ>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 1 ? 3 : 2))) void la_sum_kernel(
     const LaArgs a) {
   using T = typename Io<IO>::T;
   using TileK = Tile<IO, KD, kThreads>;
   using TileV = Tile<IO, kVS, kThreads>;
-  // float32 tiles once, with a second barrier: two workgroups on a CU instead of one
-  constexpr int kTBuf = IO == 1 ? 2 : 1, kAhead = IO == 0 && KD == 128 ? 1 : 2;
-  constexpr uint32_t kBufV = kTBuf * TileK::kBytes;
-  __shared__ __attribute__((aligned(512))) char lds[kBufV + kTBuf * TileV::kBytes];
+  constexpr uint32_t kBufV = TileK::kBytes;
+  __shared__ __attribute__((aligned(512))) char lds[kBufV + TileV::kBytes];
   __shared__ float w_in[kC];
 
   const Place pl = place(a, a.nseg - 1);
@@ -812,51 +807,41 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 
   const Rows vr = rows_of<T>(R.v, pl, rep, vd, v0, kVS, first, rev);
   const bool three = __builtin_amdgcn_readfirstlane(R.state_out != nullptr) != 0;
 
-  TileK kt[kAhead];
-  TileV vt[kAhead];
-  Ids ids[2];
+  TileK kt;
+  TileV vt;
+  Ids ids;
   const typename TileK::Ways way_k(kr, tid);
   const typename TileV::Ways way_v(vr, tid);
-  auto fetch = [&](int c, TileK& k, TileV& v) {
+  auto fetch = [&](int c) {
     const int n = c < c1 ? kC : 0;
-    k.load(kr, way_k, c, n);
-    v.load(vr, way_v, c, n);
+    kt.load(kr, way_k, c, n);
+    vt.load(vr, way_v, c, n);
   };
-  fetch(c0, kt[0], vt[0]);
-  if (kAhead == 2) fetch(c0 + 1, kt[kAhead - 1], vt[kAhead - 1]);
-  if (SEQ) ids[0].load(a.seq_idx, first, rev, c0, seqlen, lane);
+  fetch(c0);
+  if (SEQ) ids.load(a.seq_idx, first, rev, c0, seqlen, lane);
   if (tid < kC) w_in[tid] = power(g2, kC - R.off - tid) * R.sc_kv;
   const float keep = power(g2, kC);
   State<KD> S;
   S.zero();
   bool seen = false;  // a document began in this segment
-  kt[0].store(lds, tid);
-  vt[0].store(lds + kBufV, tid);
+  kt.store(lds, tid);
+  vt.store(lds + kBufV, tid);
   __syncthreads();
-  auto chunk = [&](int c, auto parity) {
-    constexpr int par = decltype(parity)::value;
-    const char* const Vs = lds + kBufV + par % kTBuf * TileV::kBytes;
-    fetch(c + kAhead, kt[par % kAhead], vt[par % kAhead]);
-    const uint64_t begins = SEQ && c < c1 ? ids[par].begins() : 0;
+  for (int c = c0; c < c1; ++c) {
+    fetch(c + 1);
+    const uint64_t begins = SEQ ? ids.begins() : 0;
     seen |= begins != 0;
-    if (SEQ) ids[par ^ 1].load(a.seq_idx, first, rev, c + 1, seqlen, lane);
-    if (c < c1) {
-      uint32_t at_col = TileK::col_base(l15, g), at_v = TileV::col_base(l15, g) ^ TileV::col_step(wv);
-      asm volatile("" : "+v"(at_col), "+v"(at_v));  // renewed, as in la_kernel
-      Op<IO> vf[2];
+    if (SEQ) ids.load(a.seq_idx, first, rev, c + 1, seqlen, lane);
+    uint32_t at_col = TileK::col_base(l15, g), at_v = TileV::col_base(l15, g) ^ TileV::col_step(wv);
+    asm volatile("" : "+v"(at_col), "+v"(at_v));  // renewed, as in la_kernel
+    Op<IO> vf[2];
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) vf[kb] = TileV::col(Vs, at_v, 0, kb);
-      const char* Ks = lds + par % kTBuf * TileK::kBytes;
-      S.template add<IO, SEQ, TileK>(Ks, at_col, vf, w_in, keep, begins, g, three);
-    }
-    if (kTBuf == 1) __syncthreads();
-    kt[(par ^ 1) % kAhead].store(lds + (par ^ 1) % kTBuf * TileK::kBytes, tid);
-    vt[(par ^ 1) % kAhead].store(lds + kBufV + (par ^ 1) % kTBuf * TileV::kBytes, tid);
+    for (int kb = 0; kb < 2; ++kb) vf[kb] = TileV::col(lds + kBufV, at_v, 0, kb);
+    S.template add<IO, SEQ, TileK>(lds, at_col, vf, w_in, keep, begins, g, three);
     __syncthreads();
-  };
-  for (int c = c0; c < c1; c += 2) {  // the second of the last two may be empty
-    chunk(c, std::integral_constant<int, 0>{});
-    chunk(c + 1, std::integral_constant<int, 1>{});
+    kt.store(lds, tid);
+    vt.store(lds + kBufV, tid);
+    __syncthreads();
   }
   float* w = a.ws + ws_base<KD>(a, pl, pl.seg + 1);
 #pragma unroll
