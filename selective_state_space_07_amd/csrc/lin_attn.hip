@@ -34,6 +34,8 @@
 // as the float32 ones: every operand is the sum of three bfloat16 parts of 8
 // significant bits each, which hold a float32 whole, and a product takes the
 // six products of parts that reach above 2^-24 of it.
+#include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "linattn_internal.h"
@@ -50,7 +52,8 @@ constexpr int kThreads = 256;  // four waves of 16 columns: the state's task
 constexpr int kMaxRoles = 3;
 
 struct LaArgs {
-  int32_t batch, seqlen, nheads, ngroups, nseg, seg_chunks, nroles, nsl;
+  int32_t batch, seqlen, nheads, ngroups, nseg, seg_chunks, nroles, nsl;  // nsl: column slices of the widest role
+  int32_t nslices;                                                         // of all roles
   const int32_t* seq_idx;
   const float* log_decay;
   float* ws;         // segment states
@@ -319,24 +322,27 @@ struct Tile {
 // Where a workgroup works. Ids are dealt to the eight XCDs in turn; the
 // workgroups that read the same q and k (the column slices and heads of one
 // group, and the roles) follow one another on one XCD and share its L2.
+__host__ __device__ __forceinline__ int slices(int vd) { return (vd + kVS - 1) / kVS; }
 struct Place {
   int role, slice, b, h, seg;
   bool live;
 };
 __device__ __forceinline__ Place place(const LaArgs& a, int nseg) {
-  const int id = blockIdx.x, rep = a.nheads / a.ngroups, sub = a.nroles * rep * a.nsl;
+  const int id = blockIdx.x, rep = a.nheads / a.ngroups, sub = rep * a.nslices;
   const int j = id >> 3;
   int s = j % sub;
   const int unit = (j / sub) * 8 + (id & 7);
   Place p;
   p.live = unit < a.batch * a.ngroups * nseg;
-  p.role = s % a.nroles;
-  s /= a.nroles;
-  p.slice = s % a.nsl;
+  const int h = s / a.nslices;
+  s -= h * a.nslices;
+  p.role = 0;
+  for (int n; p.role + 1 < a.nroles && s >= (n = slices(a.role[p.role].vd)); ++p.role) s -= n;
+  p.slice = s;
   const int bg = unit / nseg;
   p.seg = unit - bg * nseg;
   p.b = bg / a.ngroups;
-  p.h = (bg - p.b * a.ngroups) * rep + s / a.nsl;
+  p.h = (bg - p.b * a.ngroups) * rep + h;
   return p;
 }
 
@@ -494,7 +500,6 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
   const LaRole& R = a.role[pl.role];
   int kd = R.kd, vd = R.vd;
   const int v0 = pl.slice * kVS;
-  if (v0 >= vd) return;
   // kept in scalar registers, not loaded again in the loop
   float sc_out = R.sc_out, sc_kv = R.sc_kv;
   void* out_p = R.out;
@@ -795,7 +800,6 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 
   if (!pl.live) return;
   const LaRole& R = a.role[pl.role];
   const int kd = R.kd, vd = R.vd, v0 = pl.slice * kVS, seqlen = a.seqlen;
-  if (v0 >= vd) return;
   const bool rev = R.rev;
   const int tid = threadIdx.x, lane = tid & 63, l15 = lane & 15, g = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -894,7 +898,7 @@ __global__ __launch_bounds__(kThreads) void la_join_kernel(const LaArgs a) {
 
 template <int IO, int KD, bool SEQ>
 hipError_t launch_typed(const LaCall& c, const LaPlan& p, const LaArgs& a) {
-  const int64_t sub = static_cast<int64_t>(a.nroles) * (a.nheads / a.ngroups) * a.nsl;
+  const int64_t sub = static_cast<int64_t>(a.nheads / a.ngroups) * a.nslices;
   auto grid = [&](int nseg) {
     const int64_t units = static_cast<int64_t>(a.batch) * a.ngroups * nseg;
     return dim3(static_cast<unsigned>((units + 7) / 8 * 8 * sub));
@@ -915,26 +919,42 @@ hipError_t launch_typed(const LaCall& c, const LaPlan& p, const LaArgs& a) {
 int padded(int32_t d) { return d <= 64 ? 64 : 128; }
 
 size_t state_floats(const LaPlan& p, int32_t batch, int32_t nheads, int32_t kd, int32_t vd, int32_t nroles) {
-  const size_t nsl = (vd + kVS - 1) / kVS;
-  return static_cast<size_t>(nroles) * batch * nheads * p.nseg * nsl * padded(kd) * kVS;
+  return static_cast<size_t>(nroles) * batch * nheads * p.nseg * slices(vd) * padded(kd) * kVS;
 }
 
 }  // namespace
 
-LaPlan la_plan(int32_t batch, int32_t seqlen, int32_t nheads, int32_t d_k, int32_t d_v, int32_t nroles) {
+// One workgroup per CU is resident, so the sums of a call run in rounds of 32
+// workgroups on each XCD, and segments fill the rounds where sequences are few.
+// Splitting reads k and v once more: the number of segments with the least
+// estimated time is taken, in chunks of one workgroup. A workgroup costs two
+// beside its own, a chunk of the segment sums 0.6 (they are as long as the
+// segment, or as all of them take at the rate of a CU), the join 2 and an eighth
+// for each segment. Measured: 8 x 2048, 12 heads of 128, bf16, 192 workgroups,
+// 60 us in one segment (107 in four, with an earlier kernel); 1 x 65536, 24
+// workgroups, 324 us in 21 segments, 327 in 32, 341 in 10; 2 x 4133, 24 heads of
+// 64 x 96, float32, packed, 96 workgroups, 153 us in 5, 161 in 8, 193 in 2.
+LaPlan la_plan(int32_t batch, int32_t seqlen, int32_t nheads, int32_t ngroups, int32_t d_k, int32_t d_v, int32_t nroles) {
   const int32_t nchunks = (seqlen + kC - 1) / kC;
-  const int64_t groups = static_cast<int64_t>(nroles) * batch * nheads * ((d_v + kVS - 1) / kVS);
-  // One workgroup per CU is resident where the heads are wide, three where the
-  // state alone is summed. Splitting reads k and v once more, so heads enough
-  // for five CUs in eight go unsplit (8 x 2048, 12 heads of 128, 192
-  // workgroups: 69 us, 107 split in four), and fewer are split into three
-  // rounds (1 x 65536, 24 workgroups: 357 us in 32 segments, 436 in 8).
-  const int64_t want = groups >= 160 ? 1 : 768 / groups, most = nchunks / 4 > 1 ? nchunks / 4 : 1;
-  const int32_t nseg = static_cast<int32_t>(want < most ? want : most);
-  LaPlan p;
-  p.seg_chunks = (nchunks + nseg - 1) / nseg;
-  p.nseg = (nchunks + p.seg_chunks - 1) / p.seg_chunks;
-  return p;
+  const int64_t units = static_cast<int64_t>(batch) * ngroups;
+  // a backward call makes d_k columns twice and d_v columns once
+  const int64_t sub = static_cast<int64_t>(nheads / ngroups) * (nroles == 1 ? slices(d_v) : 2 * slices(d_k) + slices(d_v));
+  // workgroups of the fullest CU
+  auto load = [&](int64_t nseg) { return static_cast<double>((units * nseg + 7) / 8 * sub) / 32; };
+  LaPlan best{1, nchunks};
+  double least = 0;
+  for (int32_t n = 1; n <= 256 && (n == 1 || n <= nchunks / 4); ++n) {
+    const int32_t len = (nchunks + n - 1) / n;
+    if (n > 1 && (nchunks + len - 1) / len != n) continue;  // as many segments as a smaller n
+    double t = std::ceil(load(n)) * (len + 2);
+    if (n > 1) t += 2 + n / 8.0 + 0.6 * len * std::max(load(n - 1), 1.0);
+    if (n == 1 || t < least) {
+      least = t;
+      best.nseg = n;
+      best.seg_chunks = len;
+    }
+  }
+  return best;
 }
 
 size_t la_ws_floats(const LaPlan& p, int32_t batch, int32_t nheads, int32_t d_k, int32_t d_v, int32_t nroles) {
@@ -961,7 +981,8 @@ hipError_t launch_la(const LaCall& c, const LaPlan& p) {
     kd = kd > c.role[r].kd ? kd : c.role[r].kd;
     vd = vd > c.role[r].vd ? vd : c.role[r].vd;
   }
-  a.nsl = (vd + kVS - 1) / kVS;
+  a.nsl = slices(vd);
+  for (int r = 0; r < c.nroles; ++r) a.nslices += slices(c.role[r].vd);
   a.flags = reinterpret_cast<int32_t*>(c.workspace);
   a.ws = c.workspace + (static_cast<size_t>(c.nroles) * c.batch * p.nseg + 63) / 64 * 64;
   const bool wide = padded(kd) == 128;

@@ -73,11 +73,10 @@ int check_workspace(const void* workspace, size_t bytes, size_t need) {
 }
 
 mscan::LaPlan plan_fwd(const Dims& d) {
-  return mscan::la_plan(d.batch, d.seqlen, d.nheads, d.d_k, d.d_v, 1);
+  return mscan::la_plan(d.batch, d.seqlen, d.nheads, d.ngroups, d.d_k, d.d_v, 1);
 }
 mscan::LaPlan plan_bwd(const Dims& d) {
-  const int32_t most = d.d_k > d.d_v ? d.d_k : d.d_v;
-  return mscan::la_plan(d.batch, d.seqlen, d.nheads, most, most, 3);
+  return mscan::la_plan(d.batch, d.seqlen, d.nheads, d.ngroups, d.d_k, d.d_v, 3);
 }
 size_t fwd_floats(const Dims& d) { return mscan::la_ws_floats(plan_fwd(d), d.batch, d.nheads, d.d_k, d.d_v, 1); }
 // The backward's workspace: segment states, then dq and dk of every head.

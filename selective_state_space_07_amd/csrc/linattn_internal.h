@@ -47,7 +47,7 @@ struct LaCall {
 struct LaPlan {
   int32_t nseg, seg_chunks;
 };
-LaPlan la_plan(int32_t batch, int32_t seqlen, int32_t nheads, int32_t d_k, int32_t d_v, int32_t nroles);
+LaPlan la_plan(int32_t batch, int32_t seqlen, int32_t nheads, int32_t ngroups, int32_t d_k, int32_t d_v, int32_t nroles);
 // Workspace floats of the segment states and flags (0 for one segment).
 size_t la_ws_floats(const LaPlan& p, int32_t batch, int32_t nheads, int32_t d_k, int32_t d_v, int32_t nroles);
 hipError_t launch_la(const LaCall& c, const LaPlan& p);
