@@ -475,8 +475,11 @@ struct Plan {
   static constexpr int kKV = TileK::kBytes + TileV::kBytes, kS = TileS::kBytes, kMost = 160 * 1024 - 1024;
   static constexpr int kTBuf = 2 * kKV + kS <= kMost ? 2 : 1, kSBuf = 2 * kKV + 2 * kS <= kMost ? 2 : 1;
   static_assert(kTBuf * kKV + kSBuf * kS <= kMost, "LDS");
-  // chunks that K, V and Q are ahead in registers: two, or one where two do not fit
-  static constexpr int kAhead = IO == 0 && KD == 128 ? 1 : 2;
+  // Chunks that K, V and Q are ahead in registers: two, but one where two would
+  // spill (float32 128 wide: gradients of 2 x 1501 packed 160 us, 228 with two)
+  // and where two workgroups share a CU and its registers (bfloat16 64 wide:
+  // 8 x 2048, 24 heads, 50 us either way, packed gradients 140 us, 146 with two).
+  static constexpr int kAhead = (IO == 0) == (KD == 128) ? 1 : 2;
 };
 
 template <int IO, int KD, bool SEQ>
@@ -681,7 +684,7 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
         qf[kb] = split<3>(lo, hi);
       }
     }
-    if (kAhead == 1) fetch_q(c + 1, q[0]);  // what it held is in the parts
+    if (kAhead == 1) fetch_q(c + 1, q[0]);  // what it held is in the operands
     f4 y[4];  // columns t, rows spread(i, 4 g) + r of the 64 columns of v
     if (c < c1) {
       // the scores: columns t, rows s; tiles 0 and 1 have s < 32, the other two are needed by the upper 32 tokens
