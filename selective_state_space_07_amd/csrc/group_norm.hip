@@ -16,8 +16,8 @@
 // memory traffic, and by how much of it is under way. A group of up to 512
 // bytes' worth of 16-byte pieces, one a lane, is held by 1 to 64 lanes of one
 // wave, which takes several neighbouring groups and several rows at a time; a
-// larger one by a workgroup of up to 16 waves, one or a few pieces a lane,
-// whose waves' sums meet in LDS (a wave that held all of 1536 channels would
+// larger one by a workgroup of up to 16 waves, one piece a lane,
+// whose waves' sums meet in LDS (the largest are read anew instead; a wave that held all of 1536 channels would
 // need 300 registers in the backward and leave its SIMD with one wave). The
 // mean is taken first and the squares of what is left of it, in float32.
 // Lanes keep their channels from row to row, so that the sums over rows stay
@@ -407,6 +407,150 @@ __global__ __launch_bounds__(WIDE ? 1024 : 64 * kWaves) void gnorm_kernel(const 
   }
 }
 
+// A group of more values than one piece (4 single elements) a thread, 16 at the
+// most: it is not kept. Every pass reads it again, from the caches (a row of
+// three such tensors is at most 192 KB), piece by piece, and only the sums over
+// rows stay in registers. Held whole, a lane's values left 300 to 750 bytes in
+// scratch memory: gradients of 1024 x 16384, one group, 151 us in bfloat16 and
+// 230 in float32, 95 and 133 so; forward 33 and 47 us, 31 and 66 so.
+template <int IO, int V, bool BWD>
+__global__ __launch_bounds__(1024) void gnorm_large_kernel(const GnArgs a) {
+  using T = typename Io<IO>::T;
+  constexpr int K = 16 / V;
+  __shared__ float red[2][2][16];
+  const int lanes = static_cast<int>(blockDim.x);
+  const int ch0 = static_cast<int>(blockIdx.x % a.tiles) * a.gs, blk = blockIdx.x / a.tiles;
+  const float inv = 1.0f / static_cast<float>(a.gs);
+  int half = 0;
+  auto sum = [&](float v0, float v1, float (&v)[2]) {
+    v[0] = v0;
+    v[1] = v1;
+    wide_sum(v, red, half);
+    half ^= 1;
+  };
+  float sw[BWD ? K : 1][V], sb[BWD ? K : 1][V];
+  if constexpr (BWD) {
+#pragma unroll
+    for (int p = 0; p < K; ++p)
+#pragma unroll
+      for (int i = 0; i < V; ++i) sw[p][i] = sb[p][i] = 0.0f;
+  }
+  // f(piece, first channel of the group) for the thread's pieces, one by one
+  auto pieces = [&](auto&& f) {
+#pragma unroll
+    for (int p = 0; p < K; ++p) {
+      int t = threadIdx.x;
+      asm volatile("" : "+v"(t)::"memory");  // its places and loads not before the last piece's use
+      const int e = (p * lanes + t) * V;
+      if (e < a.gs) f(p, e);
+    }
+  };
+  for (int64_t row = blk; row < a.rows; row += a.nblk) {
+    const int64_t at_x = row * a.x_row + ch0, at_z = row * a.z_row + ch0, at_dy = row * a.dy_row + ch0;
+    const int64_t out = row * a.channels + ch0;
+    // the values of a piece before their norm (gated, where the gate is first)
+    auto read = [&](int e, float (&x)[V], float (&z)[V], float (&u)[V]) {
+      unpack<IO, V>(fetch<IO, V>(a.x, at_x + e, true), x);
+      if (a.gate != kGateNone) unpack<IO, V>(fetch<IO, V>(a.z, at_z + e, true), z);
+#pragma unroll
+      for (int i = 0; i < V; ++i) u[i] = a.gate == kGateFirst ? x[i] * act(a.activation, z[i]) : x[i];
+    };
+    float x[V], z[V], u[V], v[2], mu = 0.0f, t = 0.0f;
+    if (a.center) {
+      pieces([&](int, int e) {
+        read(e, x, z, u);
+#pragma unroll
+        for (int i = 0; i < V; ++i) t += u[i];
+      });
+      sum(t, 0.0f, v);
+      mu = v[0] / static_cast<float>(a.gs);  // divided: see above
+    }
+    t = 0.0f;
+    pieces([&](int, int e) {
+      read(e, x, z, u);
+#pragma unroll
+      for (int i = 0; i < V; ++i) t = fmaf(u[i] - mu, u[i] - mu, t);
+    });
+    sum(t, 0.0f, v);
+    const float r = __builtin_amdgcn_rsqf(fmaf(v[0], inv, a.eps));
+    float w[V], b[V];
+    if constexpr (!BWD) {
+      pieces([&](int, int e) {
+        read(e, x, z, u);
+        fetch_params<V>(a.weight, ch0 + e, true, 1.0f, w);
+        fetch_params<V>(a.bias, ch0 + e, true, 0.0f, b);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          u[i] = fmaf((u[i] - mu) * r, w[i], b[i]);
+          if (a.gate == kGateAfter) u[i] *= act(a.activation, z[i]);
+          if (a.gate == kGateNone) u[i] = act(a.activation, u[i]);
+        }
+        put<IO, V>(static_cast<T*>(a.out) + out + e, u);
+      });
+    } else {
+      // u becomes xh, d becomes dn, and z the factor of dz (gate after: dz itself)
+      float d[V];
+      auto grads = [&](int e) {
+        read(e, x, z, u);
+        unpack<IO, V>(fetch<IO, V>(a.dy, at_dy + e, true), d);
+        fetch_params<V>(a.weight, ch0 + e, true, 1.0f, w);
+        fetch_params<V>(a.bias, ch0 + e, true, 0.0f, b);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          u[i] = (u[i] - mu) * r;
+          if (a.gate == kGateFirst) continue;
+          const float n = fmaf(u[i], w[i], b[i]);
+          float g;
+          const float da = act_grad(a.activation, a.gate == kGateNone ? n : z[i], g);
+          if (a.gate == kGateAfter) z[i] = d[i] * n * da;
+          d[i] *= a.gate == kGateNone ? da : g;
+        }
+      };
+      float m0 = 0.0f, m1 = 0.0f;
+      pieces([&](int p, int e) {
+        grads(e);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          sw[p][i] = fmaf(d[i], u[i], sw[p][i]);
+          sb[p][i] += d[i];
+          m0 = fmaf(d[i], w[i], m0);
+          m1 = fmaf(d[i] * w[i], u[i], m1);
+        }
+      });
+      sum(m0, m1, v);
+      m0 = a.center ? v[0] * inv : 0.0f;
+      m1 = v[1] * inv;
+      pieces([&](int, int e) {
+        grads(e);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          d[i] = r * (d[i] * w[i] - m0 - u[i] * m1);
+          if (a.gate == kGateFirst) {
+            float g;
+            z[i] = act_grad(a.activation, z[i], g) * d[i] * x[i];
+            d[i] *= g;
+          }
+        }
+        put<IO, V>(static_cast<T*>(a.out) + out + e, d);
+        if (a.gate != kGateNone) put<IO, V>(static_cast<T*>(a.dz) + out + e, z);
+      });
+    }
+  }
+  if constexpr (BWD) {
+#pragma unroll
+    for (int p = 0; p < K; ++p) {
+      const int e = (p * lanes + static_cast<int>(threadIdx.x)) * V;
+      if (e >= a.gs) continue;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int64_t at = static_cast<int64_t>(blk) * a.channels + ch0 + e + i;
+        if (a.pw) a.pw[at] = sw[p][i];
+        if (a.pb) a.pb[at] = sb[p][i];
+      }
+    }
+  }
+}
+
 // out[c] = sum over blocks of part[block][c]: 16 channels a workgroup, whose 64
 // quarter waves take every 64th block, four at a time.
 __global__ __launch_bounds__(1024) void gnorm_sum_kernel(int32_t nblk, int32_t channels, const float* pw,
@@ -450,7 +594,7 @@ Layout layout(int32_t channels, int32_t groups, int32_t io_dtype, bool can_vec, 
   l.rp = 1;
   l.u = 1;
   if (l.wide) {
-    // whole waves, of as few pieces a lane as 16 of them allow
+    // whole waves, of as few pieces a lane as 16 of them allow; 16 values a lane: gnorm_large_kernel
     l.k = l.vec == 1 ? (pieces <= 4096 ? 4 : 16) : pieces <= 1024 ? 1 : io_dtype == 0 ? 4 : 2;
     l.threads = ((pieces + l.k - 1) / l.k + 63) / 64 * 64;
     l.ln = l.threads;
@@ -504,15 +648,23 @@ hipError_t launch_typed(const GnCall& c, const Layout& l, const GnArgs& a) {
   return launch_gate<IO, V, K, UF, UB, WIDE, kGateFirst>(c, l, a);
 }
 
+template <int IO, int V>
+hipError_t launch_large(const GnCall& c, const Layout& l, const GnArgs& a) {
+  const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(l.tiles) * a.nblk)), block(l.threads);
+  if (c.dy)
+    hipLaunchKernelGGL((gnorm_large_kernel<IO, V, true>), grid, block, 0, c.stream, a);
+  else
+    hipLaunchKernelGGL((gnorm_large_kernel<IO, V, false>), grid, block, 0, c.stream, a);
+  return hipGetLastError();
+}
+
 template <int IO>
 hipError_t launch_io(const GnCall& c, const Layout& l, const GnArgs& a) {
   constexpr int V = IO == 0 ? 4 : 8;
   if (l.wide) {
     if (l.vec == 1)
-      return l.k == 4 ? launch_gate<IO, 1, 4, 1, 1, true, kGateAny>(c, l, a)
-                      : launch_gate<IO, 1, 16, 1, 1, true, kGateAny>(c, l, a);
-    return l.k == 1 ? launch_typed<IO, V, 1, 1, 1, true>(c, l, a)
-                    : launch_gate<IO, V, 16 / V, 1, 1, true, kGateAny>(c, l, a);
+      return l.k == 4 ? launch_gate<IO, 1, 4, 1, 1, true, kGateAny>(c, l, a) : launch_large<IO, 1>(c, l, a);
+    return l.k == 1 ? launch_typed<IO, V, 1, 1, 1, true>(c, l, a) : launch_large<IO, V>(c, l, a);
   }
   if (l.vec == 1)
     return l.k == 2 ? launch_typed<IO, 1, 2, 1, 1, false>(c, l, a) : launch_gate<IO, 1, 8, 1, 1, false, kGateAny>(c, l, a);

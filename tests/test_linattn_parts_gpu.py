@@ -1,0 +1,105 @@
+"""Linear attention on the GPU where its arithmetic and its split could go
+wrong: float32 operands as three bfloat16 parts, over magnitudes far apart;
+sequences in several segments, with the roles of a backward call of different
+widths; infinities behind a token in its own chunk; float32 rows as far apart as
+they may be.
+
+Bounds as in test_linattn_gpu.py, counted anew for the parts: a float32 is the
+sum of three roundings to bfloat16, each at most 2^-9 of what is left, so the
+parts are within 2^-27 of it; of a product's nine partial products the three
+smallest are left out, 2 * 2^-9 * 2^-18 + 2^-36 < 2^-25 of it; and its six others
+are added one by one, six roundings where one was counted: 6 c + 4 instead of c."""
+import numpy as np
+import pytest
+import torch
+
+import selective_state_space_07_amd as ms
+from oracle import linattn as la
+from tests.test_linattn_gpu import absolute, bwd_args, check_bwd, check_fwd, DT, fwd_args, gpu, make, steps, U
+
+pytestmark = pytest.mark.gpu
+
+
+def spread_out(a):
+    """The columns of q, k and v (and of their partners) scaled by powers of two from 2^-40 to 2^40, q against k."""
+    dk, dv = a["k"].shape[3], a["v"].shape[3]
+    ek = torch.exp2(torch.linspace(-40, 40, dk).round())
+    ev = torch.exp2(torch.linspace(40, -40, dv).round())
+    a["q"], a["k"], a["v"] = a["q"] / ek, a["k"] * ek, a["v"] * ev
+    a["state"] = a["state"] * ev[:, None] * ek
+    a["dy"] = a["dy"] / ev
+    a["dstate"] = a["dstate"] / (ev[:, None] * ek)
+    return a
+
+
+@pytest.mark.parametrize("docs", [0, 50], ids=["one", "packed"])
+@pytest.mark.parametrize("shape", [(1, 150, 2, 1, 64, 64), (2, 130, 2, 2, 128, 96)], ids=str)
+def test_float32_keeps_its_24_bits(shape, docs):
+    a = spread_out(make(*shape, torch.float32, seed=31, state=True, docs=docs, backward=True))
+    d = gpu(a)
+    got = ms.lin_attn_fwd(*fwd_args(d), seq_idx=d["seq_idx"])
+    grads = ms.lin_attn_bwd(*bwd_args(d), seq_idx=d["seq_idx"])
+    torch.cuda.synchronize()
+    kw = dict(seq_idx=a["seq_idx"])
+    want, size = la.oracle_fwd(*fwd_args(a), **kw), la.oracle_fwd(*fwd_args(absolute(a)), **kw)
+    gwant, gsize = la.oracle_bwd(*bwd_args(a), **kw), la.oracle_bwd(*bwd_args(absolute(a)), **kw)
+    pairs = [(got[0], want[0], size[0], "y"), (got[1], want[1], size[1], "state")]
+    pairs += [(grads[n], gwant[n], gsize[n], n) for n in grads]
+    for g, w, s, what in pairs:
+        err = np.abs(g.cpu().double().numpy() - w)
+        assert (err <= (6 * steps(a) + 4) * U * s).all(), what
+        # and in the mean as a float32 product would: far below one part's or two parts' 2^-9 and 2^-17
+        assert (err / s).mean() < 16 * U, what
+
+
+@pytest.mark.parametrize("docs", [0, 300], ids=["one", "packed"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(2, 1501, 6, 3, 64, 96), (1, 2100, 2, 1, 128, 40), (1, 4099, 1, 1, 24, 128),
+                                   (1, 1025, 3, 3, 128, 128)], ids=str)
+def test_segments(shape, dtype, docs):
+    assert ms.lin_attn_workspace_bytes(*shape, DT[dtype]) > 0
+    a = make(*shape, DT[dtype], seed=32, state=True, docs=docs, backward=True)
+    d = gpu(a)
+    got = ms.lin_attn_fwd(*fwd_args(d), seq_idx=d["seq_idx"])
+    grads = ms.lin_attn_bwd(*bwd_args(d), seq_idx=d["seq_idx"])
+    torch.cuda.synchronize()
+    check_fwd(a, got, "%s %s" % (shape, dtype))
+    check_bwd(a, grads, "%s %s" % (shape, dtype))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("at", [64, 69, 83, 101, 127])
+def test_a_later_key_or_value_leaves_no_trace(at, bad, dtype):
+    """One token of the second chunk is not finite: those before it, in its own chunk too, stay as they are."""
+    a = make(1, 200, 2, 1, 64, 72, DT[dtype], seed=33, state=True)
+    d = gpu(a)
+    y0, _ = ms.lin_attn_fwd(*fwd_args(d))
+    for n in ("k", "v"):
+        e = dict(d, **{n: d[n].clone()})
+        e[n][0, at, 0, 5] = bad
+        y1, _ = ms.lin_attn_fwd(*fwd_args(e))
+        torch.cuda.synchronize()
+        # where the sums are taken again they are taken one by one: float32 roundings, and one of the output
+        tol = dict(rtol=2e-5, atol=2e-5) if dtype == "f32" else dict(rtol=2.0 ** -7, atol=2.0 ** -7)
+        torch.testing.assert_close(y1[:, :at], y0[:, :at], **tol)
+        assert not torch.isfinite(y1[0, at, 0]).all()
+
+
+def test_float32_rows_as_far_apart_as_they_may_be():
+    """2^24 elements from row to row: a chunk's offsets fill 32 bits."""
+    L, dk, dv = 150, 40, 72
+    wide = torch.empty(1, L, 1 << 24, dtype=torch.float32, device="cuda")
+    a = make(1, L, 1, 1, dk, dv, torch.float32, seed=34, backward=True)
+    d, at = {}, 0
+    for n in ("q", "k", "v", "dy"):
+        w = a[n].shape[3]
+        d[n] = wide[..., at:at + w].view(1, L, 1, w)
+        d[n].copy_(a[n])
+        at += w
+    g = a["log_decay"].cuda()
+    got = ms.lin_attn_fwd(d["q"], d["k"], d["v"], g)
+    grads = ms.lin_attn_bwd(d["q"], d["k"], d["v"], g, d["dy"])
+    torch.cuda.synchronize()
+    check_fwd(a, got, "wide rows")
+    check_bwd(a, grads, "wide rows")
