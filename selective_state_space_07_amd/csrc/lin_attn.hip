@@ -85,27 +85,48 @@ struct Parts {
 template <int IO>
 using Op = Parts<IO == 1 ? 1 : 3>;
 
-// Two values as one word of bfloat16, which is taken off them: each part of a
-// value is the rounded rest of those before it.
-__device__ __forceinline__ uint32_t take(float& a, float& b) {
-  typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
-  const uint32_t w = __builtin_bit_cast(uint32_t, bf2{static_cast<__bf16>(a), static_cast<__bf16>(b)});
-  a -= __uint_as_float(w << 16);
-  b -= __uint_as_float(w & 0xFFFF0000u);
+// Two values as one word of bfloat16, and what the rounding left of them: each
+// part of a value is the rounded rest of those before it. The word is opaque,
+// or the compiler would round the two one by one, to unpack them from there.
+typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  uint32_t w = __builtin_bit_cast(uint32_t, bf2{static_cast<__bf16>(a), static_cast<__bf16>(b)});
+  asm("" : "+v"(w));
   return w;
 }
-__device__ __forceinline__ bf8 take(float (&x)[8]) {
-  u4 w;
+__device__ __forceinline__ void rest2(float& a, float& b, uint32_t w) {
+  a -= __uint_as_float(w << 16);
+  b -= __uint_as_float(w & 0xFFFF0000u);
+}
+__device__ __forceinline__ u4 pack(const float (&x)[8]) {
+  return u4{pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7])};
+}
+__device__ __forceinline__ void rest(float (&x)[8], u4 w) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) w[j] = take(x[2 * j], x[2 * j + 1]);
-  return __builtin_bit_cast(bf8, w);
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t e = w[j];
+    rest2(x[2 * j], x[2 * j + 1], e);
+  }
+}
+// NaN once any value in w is infinite or NaN
+__device__ __forceinline__ float unfit(u4 w, float so_far) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t e = w[j];
+    so_far = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf2, e), bf2{}, so_far, false);
+  }
+  return so_far;
 }
 template <int N>
 __device__ __forceinline__ Parts<N> split(f4 lo, f4 hi) {
   float x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
   Parts<N> o;
 #pragma unroll
-  for (int p = 0; p < N; ++p) o.p[p] = take(x);
+  for (int p = 0; p < N; ++p) {
+    const u4 w = pack(x);
+    o.p[p] = __builtin_bit_cast(bf8, w);
+    rest(x, w);
+  }
   return o;
 }
 // The same of four values, two to a word.
@@ -113,7 +134,12 @@ template <int N>
 __device__ __forceinline__ void split4(f4 v, u2 (&o)[N]) {
   float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int p = 0; p < N; ++p) o[p] = u2{take(x[0], x[1]), take(x[2], x[3])};
+  for (int p = 0; p < N; ++p) {
+    const uint32_t a = pack2(x[0], x[1]), b = pack2(x[2], x[3]);
+    o[p] = u2{a, b};
+    rest2(x[0], x[1], a);
+    rest2(x[2], x[3], b);
+  }
 }
 // Element j as float32.
 template <int N>
@@ -432,16 +458,21 @@ struct State {
       for (int r = 0; r < 4; ++r) t[i][r] = SEQ && begins ? 0.0f : t[i][r] * keep;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
-      float x[8], bad = 0.0f;
+      float x[8];
       const f4 w[2] = {*reinterpret_cast<const f4*>(w_in + 32 * kb + 8 * g),
                        *reinterpret_cast<const f4*>(w_in + 32 * kb + 8 * g + 4)};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         x[j] = get(vf[kb], j) * w[j >> 2][j & 3];
         if (SEQ) x[j] = 32 * kb + 8 * g + j >= last ? x[j] : 0.0f;
-        bad = fmaf(x[j], 0.0f, bad);
       }
-      bf8 wv[2] = {take(x), take(x)};
+      const u4 first = pack(x);
+      rest(x, first);
+      if (IO == 1 && __any(unfit(first, 0.0f) != 0.0f)) {  // an infinity or NaN is whole in its first part: its rest is NaN
+        asm volatile("");                                  // a branch, not selects
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = x[j] == x[j] ? x[j] : 0.0f;
+      }
       // four tiles at a time: their operands first, then one product with each part in turn
       auto products = [&](const auto& parts) {
 #pragma unroll
@@ -457,18 +488,14 @@ struct State {
           mma_each(t + i0, kf, parts);
         }
       };
-      if (IO == 1 && __any(bad != 0.0f)) {  // an infinity or NaN is whole in its first part, and its rest is NaN
-        asm volatile("");                   // a branch, not selects
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          x[j] = x[j] == x[j] ? x[j] : 0.0f;
-          if (!(static_cast<float>(wv[1][j]) == static_cast<float>(wv[1][j]))) wv[1][j] = static_cast<__bf16>(0.0f);
-        }
+      const u4 second = pack(x);
+      const bf8 p0 = __builtin_bit_cast(bf8, first), p1 = __builtin_bit_cast(bf8, second);
+      if (IO == 0 || three) {
+        rest(x, second);
+        products(Parts<3>{{p0, p1, __builtin_bit_cast(bf8, pack(x))}});
+      } else {
+        products(Parts<2>{{p0, p1}});
       }
-      if (IO == 0 || three)
-        products(Parts<3>{{wv[0], wv[1], take(x)}});
-      else
-        products(Parts<2>{{wv[0], wv[1]}});
     }
   }
 };
