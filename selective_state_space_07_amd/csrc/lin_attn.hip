@@ -36,14 +36,14 @@
 // six products of parts that reach above 2^-24 of it.
 //
 // Measured on an MI355X, where a large copy reaches 5.2 TB/s: 8 x 2048 tokens,
-// 12 heads of 128, bfloat16: 58 us (201 MB to read and write, 3.5 TB/s; 209 us
+// 12 heads of 128, bfloat16: 57 us (201 MB to read and write, 3.5 TB/s; 209 us
 // with one task after the other, four barriers a chunk and bank conflicts), the
-// gradients 158 us (352 MB, 2.2 TB/s: 576 workgroups are two and a quarter
-// rounds of 256 CUs and take three). A chunk takes a CU about 1.7 us: its LDS
-// traffic 0.8 us at the full rate, its matrix instructions 0.5, the other
-// vector instructions 0.5, and the rest is what two waves on a SIMD cannot
-// hide of the way from a chunk's operands to its results. Two workgroups on a
-// CU would need it in 128 registers a lane; there it spills (prompt 76 us).
+// gradients 154 us (352 MB, 2.3 TB/s: 576 workgroups are two and a quarter
+// rounds of 256 CUs and take three). Both are bound by the stream of K, V, Q
+// and y: without any of the products they take 56 and 142 us, without that
+// traffic 45 and 130. Four chunks ahead instead of two changed nothing (58 and
+// 161 us). Two workgroups on a CU would need the kernel in 128 registers a
+// lane; there it spills (prompt 76 us).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -513,9 +513,9 @@ struct Plan {
   static constexpr int kTBuf = 2 * kKV + kS <= kMost ? 2 : 1, kSBuf = 2 * kKV + 2 * kS <= kMost ? 2 : 1;
   static_assert(kTBuf * kKV + kSBuf * kS <= kMost, "LDS");
   // Chunks that K, V and Q are ahead in registers: two, but one where two would
-  // spill (float32 128 wide: gradients of 2 x 1501 packed 160 us, 228 with two)
-  // and where two workgroups share a CU and its registers (bfloat16 64 wide:
-  // 8 x 2048, 24 heads, 50 us either way, packed gradients 140 us, 146 with two).
+  // spill (float32 128 wide: 8 x 2048, 12 heads, 178 us, 198 with two) and where
+  // two workgroups share a CU and its registers (bfloat16 64 wide: 8 x 2048, 24
+  // heads, packed: gradients 137 us, 145 with two; 50 and 49 us not packed).
   static constexpr int kAhead = (IO == 0) == (KD == 128) ? 1 : 2;
 };
 
@@ -825,7 +825,7 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
 
 // What each segment but the last adds to the state: the state's task alone,
 // four waves to a workgroup and two or three workgroups to a CU, so that one
-// chunk ahead suffices (1 x 65536, 12 heads of 128, bfloat16: 384 MB in 105 us,
+// chunk ahead suffices (1 x 65536, 12 heads of 128, bfloat16: 390 MB in 105 us,
 // 3.7 TB/s; 131 us with two chunks ahead, which spilled).
 template <int IO, int KD, bool SEQ>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 1 ? 3 : 2))) void la_sum_kernel(
@@ -972,9 +972,9 @@ size_t state_floats(const LaPlan& p, int32_t batch, int32_t nheads, int32_t kd, 
 // beside its own, a chunk of the segment sums 0.6 (they are as long as the
 // segment, or as all of them take at the rate of a CU), the join 2 and an eighth
 // for each segment. Measured: 8 x 2048, 12 heads of 128, bf16, 192 workgroups,
-// 58 us in one segment (107 in four, with an earlier kernel); 1 x 65536, 24
-// workgroups, 324 us in 21 segments, 327 in 32, 341 in 10; 2 x 4133, 24 heads of
-// 64 x 96, float32, packed, 96 workgroups, 153 us in 5, 161 in 8, 193 in 2.
+// 58 us in one segment, 92 in four; 1 x 65536, 24 workgroups, 321 us in 21
+// segments (313 on another day), 322 in 32, 336 in 10; 2 x 4133, 24 heads of 64
+// x 96, float32, packed, 96 workgroups, 144 us in 5, 155 in 8, 180 in 2.
 LaPlan la_plan(int32_t batch, int32_t seqlen, int32_t nheads, int32_t ngroups, int32_t d_k, int32_t d_v, int32_t nroles) {
   const int32_t nchunks = (seqlen + kC - 1) / kC;
   const int64_t units = static_cast<int64_t>(batch) * ngroups;
@@ -1055,7 +1055,7 @@ __global__ __launch_bounds__(kThreads) void la_head_sum_kernel(int64_t n, int32_
 
 // One token. A state row (one column of v) is spread over LN lanes of 4
 // k-elements each; the kernel reads and writes the state once and is bound by
-// that traffic (256 conversations, 12 heads of 128: 406 MB in 72 us, 5.6 TB/s,
+// that traffic (256 conversations, 12 heads of 128: 406 MB in 70 us, 5.8 TB/s,
 // above the rate of a large copy, for part of it stays in the last-level cache).
 template <int IO, int LN>
 __global__ __launch_bounds__(kThreads) void la_step_kernel(const LaStepCall a, int64_t rows) {
