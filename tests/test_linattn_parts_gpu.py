@@ -103,3 +103,34 @@ def test_float32_rows_as_far_apart_as_they_may_be():
     torch.cuda.synchronize()
     check_fwd(a, got, "wide rows")
     check_bwd(a, grads, "wide rows")
+
+
+@pytest.mark.parametrize("docs", [0, 60], ids=["one", "packed"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(2, 333, 3, 1, 64, 64), (1, 1300, 2, 2, 128, 128)], ids=str)
+def test_without_the_state(shape, dtype, docs):
+    """Where the state is not returned, bfloat16 values enter it in two parts: 2^-17 of each term, which the bound's
+    BF^2 = 2^-16 holds."""
+    a = make(*shape, DT[dtype], seed=35, state=True, docs=docs)
+    d = gpu(a)
+    y, s = ms.lin_attn_fwd(*fwd_args(d), seq_idx=d["seq_idx"], return_state=False)
+    torch.cuda.synchronize()
+    assert s is None
+    check_fwd(a, (y, None), "%s %s" % (shape, dtype))
+
+
+def test_an_infinite_value_without_the_state():
+    """An infinite value makes later outputs infinite, not NaN, where keys and queries are above 0; other columns
+    stay as they were."""
+    a = make(1, 200, 1, 1, 64, 64, torch.bfloat16, seed=36)
+    a["q"], a["k"] = a["q"].abs() + 1, a["k"].abs() + 1
+    d = gpu(a)
+    y0, _ = ms.lin_attn_fwd(*fwd_args(d), return_state=False)
+    d["v"] = d["v"].clone()
+    d["v"][0, 70, 0, 9] = float("-inf")
+    y1, _ = ms.lin_attn_fwd(*fwd_args(d), return_state=False)
+    torch.cuda.synchronize()
+    assert (y1[0, 70:, 0, 9] == float("-inf")).all()
+    other = torch.arange(64) != 9
+    torch.testing.assert_close(y1[..., other], y0[..., other], rtol=2.0 ** -7, atol=2.0 ** -7)
+    torch.testing.assert_close(y1[:, :70], y0[:, :70], rtol=2.0 ** -7, atol=2.0 ** -7)
