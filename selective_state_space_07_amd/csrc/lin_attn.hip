@@ -845,16 +845,41 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 
   const int tid = threadIdx.x, lane = tid & 63, l15 = lane & 15, g = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rep = a.nheads / a.ngroups;
-  const int c0 = pl.seg * a.seg_chunks, c1 = c0 + a.seg_chunks;  // whole chunks: a later segment follows
+  const int seg0 = pl.seg * a.seg_chunks, c1 = seg0 + a.seg_chunks;  // whole chunks: a later segment follows
   const float g2 = a.log_decay[pl.h] * kLog2e;
   const int64_t first = static_cast<int64_t>(pl.b) * seqlen + (rev ? seqlen - 1 : 0);
   const Rows kr = rows_of<T>(R.k, pl, rep, kd, 0, KD, first, rev);
   const Rows vr = rows_of<T>(R.v, pl, rep, vd, v0, kVS, first, rev);
   const bool three = __builtin_amdgcn_readfirstlane(R.state_out != nullptr) != 0;
+  // Only the segment's last document adds to its state: the sum starts in the
+  // chunk where that begins, found from the segment's end, 1024 tokens at a time.
+  int c0 = seg0;
+  bool seen = false;  // a document begins in this segment
+  if (SEQ) {
+    __shared__ int newest[2][kThreads / 64];
+    const int32_t* ids = a.seq_idx + first;
+    const int sign = rev ? -1 : 1;
+    for (int end = c1 * kC, half = 0; end > seg0 * kC && !seen; end -= 4 * kThreads, half ^= 1) {
+      int at = -1;
+#pragma unroll
+      for (int i = 3; i >= 0; --i) {
+        const int pos = end - 1 - i * kThreads - tid;
+        if (pos >= seg0 * kC && pos > 0)
+          at = max(at, ids[sign * static_cast<int64_t>(pos)] != ids[sign * static_cast<int64_t>(pos - 1)] ? pos : -1);
+      }
+      for (int o = 32; o > 0; o >>= 1) at = max(at, __shfl_xor(at, o, 64));
+      if (lane == 0) newest[half][wv] = at;
+      __syncthreads();
+      at = max(max(newest[half][0], newest[half][1]), max(newest[half][2], newest[half][3]));
+      seen = at >= 0;
+      if (seen) c0 = at / kC;
+    }
+    c0 = __builtin_amdgcn_readfirstlane(c0);
+  }
 
   TileK kt;
   TileV vt;
-  Ids ids;
+  Ids marks;
   const typename TileK::Ways way_k(kr, tid);
   const typename TileV::Ways way_v(vr, tid);
   auto fetch = [&](int c) {
@@ -863,20 +888,18 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 
     vt.load(vr, way_v, c, n);
   };
   fetch(c0);
-  if (SEQ) ids.load(a.seq_idx, first, rev, c0, seqlen, lane);
+  if (SEQ) marks.load(a.seq_idx, first, rev, c0, seqlen, lane);
   if (tid < kC) w_in[tid] = power(g2, kC - R.off - tid) * R.sc_kv;
   const float keep = power(g2, kC);
   State<KD> S;
   S.zero();
-  bool seen = false;  // a document began in this segment
   kt.store(lds, tid);
   vt.store(lds + kBufV, tid);
   __syncthreads();
   for (int c = c0; c < c1; ++c) {
     fetch(c + 1);
-    const uint64_t begins = SEQ ? ids.begins() : 0;
-    seen |= begins != 0;
-    if (SEQ) ids.load(a.seq_idx, first, rev, c + 1, seqlen, lane);
+    const uint64_t begins = SEQ ? marks.begins() : 0;
+    if (SEQ) marks.load(a.seq_idx, first, rev, c + 1, seqlen, lane);
     uint32_t at_col = TileK::col_base(l15, g), at_v = TileV::col_base(l15, g) ^ TileV::col_step(wv);
     asm volatile("" : "+v"(at_col), "+v"(at_v));  // renewed, as in la_kernel
     Op<IO> vf[2];

@@ -134,3 +134,33 @@ def test_an_infinite_value_without_the_state():
     other = torch.arange(64) != 9
     torch.testing.assert_close(y1[..., other], y0[..., other], rtol=2.0 ** -7, atol=2.0 ** -7)
     torch.testing.assert_close(y1[:, :70], y0[:, :70], rtol=2.0 ** -7, atol=2.0 ** -7)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [(8, 8192, 3), (8, 16384, 6)], ids=str)
+def test_where_documents_begin_in_segments(size, dtype):
+    """Segments of hundreds and of thousands of tokens, each row with beginnings of its own: at a segment's first and last
+    tokens, beside a chunk's edges, far from its end, and none at all; in both directions."""
+    (b, L, H), d = size, 8
+    for backward in (False, True):
+        a = make(b, L, H, H, d, d, DT[dtype], seed=37, state=True, backward=True)
+        n = ms.lin_attn_workspace_bytes(b, L, H, H, d, d, DT[dtype], backward=backward) // 4
+        nseg = n // ((3 if backward else 1) * b * H * 64 * 64)
+        step = -(-(L // 64) // nseg) * 64  # tokens of a segment, from the start or, backwards, from the end
+        assert nseg > 1 and step >= 256
+        edge = L - step if backward else step
+        rows = [[], [1], [edge], [edge - 1, edge + 1], [edge - 63, edge + 65], [70, L - 2], [5 * 64, L - 5 * 64],
+                [L - 1]]
+        begins = torch.zeros(b, L, dtype=torch.int32)
+        for r, at in enumerate(rows):
+            begins[r, at] = 1
+        a["seq_idx"] = begins.cumsum(1).to(torch.int32)
+        g = gpu(a)
+        if backward:
+            got = ms.lin_attn_bwd(*bwd_args(g), seq_idx=g["seq_idx"])
+            torch.cuda.synchronize()
+            check_bwd(a, got, "backward")
+        else:
+            got = ms.lin_attn_fwd(*fwd_args(g), seq_idx=g["seq_idx"])
+            torch.cuda.synchronize()
+            check_fwd(a, got, "forward")
