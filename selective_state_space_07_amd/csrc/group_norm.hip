@@ -165,30 +165,33 @@ __device__ __forceinline__ void wide_sum(float (&v)[N], float (&red)[2][N][16], 
   }
 }
 
-// sigmoid(z) and 1 - sigmoid(z), the latter without cancellation. The exponent
-// is capped at 100, where 1 + e rounds to e: e sigmoid(z) stays 1, not inf * 0.
+// sigmoid(z) = 1 / (1 + e), e = e^-z, and 1 - sigmoid(z) = e / (1 + e), the
+// latter without cancellation. Where e overflows the first is 0 and the minimum
+// takes the second from infinity times 0 to 1 (a NaN is in the first).
 struct Sig {
   float s, c;
 };
 __device__ __forceinline__ Sig sigmoid(float z) {
-  float t = -z * kLog2e;
-  t = t > 100.0f ? 100.0f : t;
-  const float e = exp2_hw(t), s = rcp_hw(1.0f + e);
-  return Sig{s, e * s};
+  const float e = exp2_hw(-z * kLog2e), s = rcp_hw(1.0f + e);
+  return Sig{s, fminf(e * s, 1.0f)};
 }
+// z sigmoid(z). Below -128 the second factor is 0 (e^128 is beyond float32),
+// and so the first may stay at -128 there: -inf closes a gate as the lowest
+// value does, not as infinity times 0.
+__device__ __forceinline__ float silu_of(float z, float s) { return fmaxf(z, -128.0f) * s; }
 // Chosen by value, not by branch: the kind is the same for a whole launch, and
 // a branch at each element would keep the elements from overlapping.
 __device__ __forceinline__ float act(int kind, float z) {
   const float s = sigmoid(z).s;
-  const float a = kind == kActSilu ? z * s : s;
+  const float a = kind == kActSilu ? silu_of(z, s) : s;
   return kind == kActNone ? z : a;
 }
-// activation and its derivative
+// activation and its derivative: of silu, s + z s (1 - s)
 __device__ __forceinline__ float act_grad(int kind, float z, float& a) {
   const Sig g = sigmoid(z);
-  const float b = kind == kActSilu ? z * g.s : g.s;
+  const float b = kind == kActSilu ? silu_of(z, g.s) : g.s;
   a = kind == kActNone ? z : b;
-  const float d = g.s * (kind == kActSilu ? fmaf(z, g.c, 1.0f) : g.c);
+  const float d = kind == kActSilu ? fmaf(b, g.c, g.s) : g.s * g.c;
   return kind == kActNone ? 1.0f : d;
 }
 
