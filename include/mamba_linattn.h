@@ -23,9 +23,9 @@
  * are not inputs (the decayed scores q.k, and S) are rounded to bfloat16; the
  * state itself is summed in float32 (w v enters its products as three bfloat16
  * parts, as two where the state is not returned). For float32 io each operand
- * is three bfloat16 parts, to float32 accuracy; there an infinity, or a finite
- * value beyond 3.38e38, may make NaN of the outputs and states that it enters,
- * and what lies below 1e-38 in a value is lost. The result equals the
+ * is three bfloat16 parts, to float32 accuracy; there an infinity may make NaN
+ * of the outputs and states that it enters, and what lies below 1e-38 in a
+ * value is lost. The result equals the
  * recurrence up to rounding and is bitwise reproducible. A token's output
  * depends only on the tokens of its own document up to it, also where others
  * hold infinities or NaN.
