@@ -426,6 +426,9 @@ struct Ids {
 __device__ __forceinline__ int last_of(uint64_t begins) { return begins ? 63 - __builtin_clzll(begins) : 0; }
 
 // S^T of one wave: column v0 + spread(wave, l15), k-elements spread(i, 4 g) + r.
+// Kernels and workspace hold half the state, which is exact, so that rounding to
+// bfloat16 takes no finite one to infinity.
+constexpr float kHalf = 0.5f;
 template <int KD>
 struct State {
   static constexpr int kTiles = KD / 16;
@@ -435,7 +438,7 @@ struct State {
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) t[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  // One head's state [vd][kd] ([kd][vd] where `transposed`), zero beyond kd.
+  // Half of one head's state [vd][kd] ([kd][vd] where `transposed`), zero beyond kd.
   __device__ __forceinline__ void load(const float* st, bool transposed, int col, int vd, int kd, int g) {
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) {
@@ -447,6 +450,7 @@ struct State {
       } else {
         t[i] = *reinterpret_cast<const f4*>(st + static_cast<int64_t>(col) * kd + e);
       }
+      t[i] *= kHalf;
     }
   }
   // S^T = lam^n S^T + K^T (w V) over the tokens of the last document; w_in
@@ -639,7 +643,7 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
     put_state(lds + kBufS);
     if (wv < 2) {
       const int n = wv == 0 ? kC : seqlen - (nchunks - 1) * kC;
-      w_in[wv][lane] = lane < n ? power(g2, n - off - lane) * sc_kv : 0.0f;
+      w_in[wv][lane] = lane < n ? power(g2, n - off - lane) * (kHalf * sc_kv) : 0.0f;
     }
     const uint32_t col_k = TileK::col_base(l15, g);
     const uint32_t col_v = TileV::col_base(l15, g) ^ TileV::col_step(wv);
@@ -666,7 +670,7 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
 #pragma unroll
       for (int i = 0; i < State<KD>::kTiles; ++i) {
         const int e = spread(i, 4 * g);
-        if (e < kd) *reinterpret_cast<f4*>(st + e) = S.t[i];
+        if (e < kd) *reinterpret_cast<f4*>(st + e) = S.t[i] * (1.0f / kHalf);
       }
     }
     return;
@@ -693,7 +697,7 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
   fetch_q(c0, q[0]);
   if (kAhead == 2) fetch_q(c0 + 1, q[kAhead - 1]);
   if (tid < 96) w_score[tid] = tid < kC ? power(g2, 63 - tid) * (sc_out * sc_kv) : 0.0f;
-  const float w_out = power(g2, 16 * wv + l15 + off) * sc_out;  // of the state read at this lane's token
+  const float w_out = power(g2, 16 * wv + l15 + off) * (sc_out / kHalf);  // of the state read at this lane's token
   const int64_t out_row = static_cast<int64_t>(nheads) * vd;
   const Rows outs{static_cast<char*>(out_p) + (first * out_row + static_cast<int64_t>(pl.h) * vd + v0) * es_out,
                   static_cast<uint32_t>(out_row * es_out), static_cast<uint32_t>(min(vd - v0, kVS) * es_out), Order{rev}};
@@ -898,7 +902,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 
   };
   fetch(c0);
   if (SEQ) marks.load(a.seq_idx, first, rev, c0, seqlen, lane);
-  if (tid < kC) w_in[tid] = power(g2, kC - R.off - tid) * R.sc_kv;
+  if (tid < kC) w_in[tid] = power(g2, kC - R.off - tid) * (kHalf * R.sc_kv);
   const float keep = power(g2, kC);
   State<KD> S;
   S.zero();
@@ -955,6 +959,7 @@ __global__ __launch_bounds__(kThreads) void la_join_kernel(const LaArgs a) {
     } else {
       s = *reinterpret_cast<const f4*>(st + static_cast<int64_t>(col) * R.kd + e);
     }
+    s *= kHalf;
   }
   const float keep = power(a.log_decay[p.h] * kLog2e, a.seg_chunks * kC);
   float* w = a.ws + ws_base<KD>(a, p, 0) + (i * kThreads + tid) * 4;

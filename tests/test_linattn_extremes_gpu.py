@@ -38,7 +38,7 @@ def close(got, want, size, a, what, rounded):
 
 
 @pytest.mark.parametrize("docs", [0, 90], ids=["one", "packed"])
-@pytest.mark.parametrize("which", ["q", "k", "v", "dy"])
+@pytest.mark.parametrize("which", ["q", "k", "v", "dy", "state", "dstate"])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("shape", [(1, 200, 2, 1, 64, 72), (1, 1100, 1, 1, 128, 40)], ids=str)
 def test_the_highest_and_lowest_values(shape, dtype, which, docs):
