@@ -27,8 +27,9 @@
  * of the outputs and states that it enters, and what lies below 1e-38 in a
  * value is lost. The result equals the
  * recurrence up to rounding and is bitwise reproducible. A token's output
- * depends only on the tokens of its own document up to it, also where others
- * hold infinities or NaN.
+ * depends only on the tokens of its own document up to it: where others hold
+ * infinities or NaN it has the bits that it has without them, and so have the
+ * gradients.
  *
  * Layouts and limits of all calls:
  *   q, k         [batch][seqlen][ngroups][d_k] io, 16-byte aligned

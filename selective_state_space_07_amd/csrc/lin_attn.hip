@@ -157,19 +157,33 @@ __device__ __forceinline__ float get(const Parts<N>& f, int j) {
   for (int p = N - 2; p >= 0; --p) v += static_cast<float>(f.p[p][j]);
   return v;
 }
-// Zero the k-values of a lane's eight that lie below `first`.
+// A lane's eight k-values where `mask` has their bits, 0 elsewhere.
 template <int N>
-__device__ __forceinline__ Parts<N> from_first(const Parts<N>& f, int first) {
+__device__ __forceinline__ Parts<N> masked(const Parts<N>& f, u4 mask) {
   Parts<N> o;
 #pragma unroll
-  for (int p = 0; p < N; ++p) {
-    u4 v = __builtin_bit_cast(u4, f.p[p]);
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      v[j] &= (2 * j >= first ? 0xFFFFu : 0u) | (2 * j + 1 >= first ? 0xFFFF0000u : 0u);
-    o.p[p] = __builtin_bit_cast(bf8, v);
-  }
+  for (int p = 0; p < N; ++p) o.p[p] = __builtin_bit_cast(bf8, __builtin_bit_cast(u4, f.p[p]) & mask);
   return o;
+}
+// Those from `first` to `last`.
+template <int N>
+__device__ __forceinline__ Parts<N> between(const Parts<N>& f, int first, int last) {
+  u4 mask;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    mask[j] = ((2 * j >= first) & (2 * j <= last) ? 0xFFFFu : 0u) |
+              ((2 * j + 1 >= first) & (2 * j + 1 <= last) ? 0xFFFF0000u : 0u);
+  return masked(f, mask);
+}
+// Those that are finite (of the others the first part is not).
+template <int N>
+__device__ __forceinline__ Parts<N> finite(const Parts<N>& f) {
+  const u4 w = __builtin_bit_cast(u4, f.p[0]);
+  u4 mask;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    mask[j] = ((w[j] & 0x7F80u) != 0x7F80u ? 0xFFFFu : 0u) | ((w[j] & 0x7F800000u) != 0x7F800000u ? 0xFFFF0000u : 0u);
+  return masked(f, mask);
 }
 // acc[i] += a[i] b over the pairs of parts that matter, the smallest first, and
 // each pair for all i in turn: consecutive products do not wait for each other.
@@ -495,7 +509,7 @@ struct State {
           // keys of other documents may hold infinities or NaN, which a weight of 0 would not remove
           if (SEQ && begins) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) kf[i] = from_first(kf[i], last - (32 * kb + 8 * g));
+            for (int i = 0; i < 4; ++i) kf[i] = between(kf[i], last - (32 * kb + 8 * g), 7);
           }
           mma_each(t + i0, kf, parts);
         }
@@ -789,24 +803,35 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
 #pragma unroll
         for (int r = 0; r < 4; ++r) bad = fmaf(y[i][r], 0.0f, bad);
       // An infinity or NaN in k or v also reaches the tokens that it is masked
-      // for, as 0 * inf. Where any sum is not finite the sums are taken again,
-      // over the unmasked tokens alone.
+      // for, as 0 * inf. Where any sum is not finite the sums are taken again, in
+      // the same order, with 0 for masked scores and for values that are not
+      // finite; the latter are added behind, where they are not masked. So a sum
+      // that none of them belongs to has the bits that it has without them.
       if (__any(bad != 0.0f)) {
-        uint32_t again = at_row;
-        asm volatile("" : "+v"(again));  // read again, not kept from above
+        uint32_t again = row_b, again_v = col_v;
+        asm volatile("" : "+v"(again), "+v"(again_v));  // read again, not kept from above
         carried(again);
+        const Op<IO> p0 = between(s0, from - 8 * gg, t - 8 * gg), p1 = between(s1, from - 8 * gg - 32, t - 8 * gg - 32);
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const Op<IO> vf[1] = {finite(TileV::col(Vs, again_v, i, kb))};
+            mma_each(y + i, vf, kb == 0 ? p0 : p1);
+          }
 #pragma unroll 1
         for (int gs = 0; gs < 4; ++gs) {
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             const int s = 32 * (k >> 3) + 8 * gs + (k & 7);
-            const float p = __shfl(k < 8 ? get(s0, k & 7) : get(s1, k & 7), 16 * gs + l15, 64);
+            const float p = __shfl(k < 8 ? get(p0, k & 7) : get(p1, k & 7), 16 * gs + l15, 64);
             if (s > t || s < from) continue;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const f4 v = TileV::get4(Vs, s, spread(i, 4 * gg));
 #pragma unroll
-              for (int r = 0; r < 4; ++r) y[i][r] = fmaf(p, v[r], y[i][r]);
+              for (int r = 0; r < 4; ++r)
+                if (v[r] * 0.0f != 0.0f) y[i][r] = fmaf(p, v[r], y[i][r]);
             }
           }
         }
