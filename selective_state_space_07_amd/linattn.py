@@ -168,6 +168,11 @@ def _sizes(q, k, v):
     return batch, seqlen, vs[2], ngroups, d_k, vs[3]
 
 
+def _scale(scale, d_k):
+    """The factor of q.k (any number for a d_k of 0, which the library refuses)."""
+    return scale if scale is not None else d_k ** -0.5 if d_k else 1.0
+
+
 def lin_attn_workspace_bytes(batch, seqlen, nheads, ngroups, d_k, d_v, dtype, backward=False):
     """Bytes of workspace `lin_attn_fwd` (or, with `backward`, `lin_attn_bwd`) needs."""
     lib = load()
@@ -198,7 +203,7 @@ def lin_attn_fwd(q, k, v, log_decay, state=None, *, scale=None, seq_idx=None, ou
     elif return_state:
         state_out = q.new_empty(state_shape, dtype=_F32)
     ws, ws_bytes, keep = scratch(workspace, lib.mamba_linattn_fwd_workspace_bytes(*sizes, io), q)
-    launch(dev, "mamba_linattn_fwd", lib, lib.mamba_linattn_fwd, *sizes, io, d_k ** -0.5 if scale is None else scale,
+    launch(dev, "mamba_linattn_fwd", lib, lib.mamba_linattn_fwd, *sizes, io, _scale(scale, d_k),
            qp, qs, kp, ks, vp, vs, ip, gp, sp, y.data_ptr(), 0 if state_out is None else state_out.data_ptr(), ws,
            ws_bytes)
     return y, state_out
@@ -231,7 +236,7 @@ def lin_attn_bwd(q, k, v, log_decay, dy, state=None, dstate=None, *, scale=None,
         grads["dstate"] = q.new_empty(state_shape, dtype=_F32)
         dsi = grads["dstate"].data_ptr()
     ws, ws_bytes, keep = scratch(workspace, lib.mamba_linattn_bwd_workspace_bytes(*sizes, io), q)
-    launch(dev, "mamba_linattn_bwd", lib, lib.mamba_linattn_bwd, *sizes, io, d_k ** -0.5 if scale is None else scale,
+    launch(dev, "mamba_linattn_bwd", lib, lib.mamba_linattn_bwd, *sizes, io, _scale(scale, d_k),
            qp, qs, kp, ks, vp, vs, ip, gp, sp, dyp, dys, dsp, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dsi, ws,
            ws_bytes)
     return grads
@@ -268,5 +273,5 @@ def lin_attn_step(q, k, v, log_decay, state, *, scale=None, inplace=False, out=N
         np = new.data_ptr()
     y = q.new_empty(v_shape) if out is None else check_out(out, "out", v_shape, dtype, q.device)
     launch(dev, "mamba_linattn_step", lib, lib.mamba_linattn_step, batch, nheads, ngroups, d_k, d_v, io,
-           d_k ** -0.5 if scale is None else scale, qp, qs, kp, ks, vp, vs, gp, sp, y.data_ptr(), np)
+           _scale(scale, d_k), qp, qs, kp, ks, vp, vs, gp, sp, y.data_ptr(), np)
     return y, new
