@@ -15,9 +15,10 @@
  *   y = n a (MAMBA_GATE_AFTER), n (MAMBA_GATE_FIRST) or act(n) (MAMBA_GATE_NONE)
  *
  * silu and its derivative are 0 at the lowest values, and at -inf as well, so
- * that either closes a gate. Each row is a sample of its own: a token's output depends on that token
- * alone. One group and center 0 is an RMS norm; with MAMBA_GATE_FIRST and silu
- * it is the norm of a Mamba-2 block behind mamba2_ssd_fwd.
+ * that either closes a gate. Each row is a sample of its own: a token's output
+ * depends on that token alone. One group and center 0 is an RMS norm; with
+ * MAMBA_GATE_FIRST and silu it is the norm of a Mamba-2 block behind
+ * mamba2_ssd_fwd.
  *
  * Statistics, sums and gradients of the parameters are float32 throughout
  * (the mean first, then the squares of the differences); outputs are rounded

@@ -165,6 +165,14 @@ __device__ __forceinline__ void wide_sum(float (&v)[N], float (&red)[2][N][16], 
   }
 }
 
+// 1 / sqrt(v). The instruction takes what lies below 2^-126 for 0, and with an
+// eps of 0 the mean square of values around 1e-20 does.
+__device__ __forceinline__ float reciprocal_root(float v) {
+  const bool low = v < 0x1p-100f;
+  const float r = __builtin_amdgcn_rsqf(low ? v * 0x1p64f : v);
+  return low ? r * 0x1p32f : r;
+}
+
 // sigmoid(z) = 1 / (1 + e), e = e^-z, and 1 - sigmoid(z) = e / (1 + e), the
 // latter without cancellation. Where e overflows the first is 0 and the minimum
 // takes the second from infinity times 0 to 1 (a NaN is in the first).
@@ -309,7 +317,7 @@ __global__ __launch_bounds__(WIDE ? 1024 : 64 * kWaves) void gnorm_kernel(const 
         for (int i = 0; i < V; ++i) s = fmaf(u[q][p][i], u[q][p][i], s);
       // 0 for the rows behind the last: with eps 0 their zeros would become NaN in the parameters' sums
       s = sum1(s);
-      r[q] = row0 + q * rp + sub < a.rows ? __builtin_amdgcn_rsqf(fmaf(s, inv, a.eps)) : 0.0f;
+      r[q] = row0 + q * rp + sub < a.rows ? reciprocal_root(fmaf(s, inv, a.eps)) : 0.0f;
     }
 
 #pragma unroll
@@ -481,7 +489,7 @@ __global__ __launch_bounds__(1024) void gnorm_large_kernel(const GnArgs a) {
       for (int i = 0; i < V; ++i) t = fmaf(u[i] - mu, u[i] - mu, t);
     });
     sum(t, 0.0f, v);
-    const float r = __builtin_amdgcn_rsqf(fmaf(v[0], inv, a.eps));
+    const float r = reciprocal_root(fmaf(v[0], inv, a.eps));
     float w[V], b[V];
     if constexpr (!BWD) {
       pieces([&](int, int e) {
