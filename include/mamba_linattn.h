@@ -14,9 +14,10 @@
  *
  * It is the recurrence of mamba2_ssd.h with a decay that depends on the head
  * alone, for any head sizes, with gradients. log_decay is meant to be <= 0
- * (-inf: no memory; values above 0 grow the state and are not refused). The
- * decays are constants of an architecture here: no gradient is defined for
- * them.
+ * (-inf: no memory). Values above 0 grow the state and are not refused; from
+ * 1.38 on lam^64 is beyond float32, and NaN may come out where the state itself
+ * would not be. The decays are constants of an architecture here: no gradient
+ * is defined for them.
  *
  * A sequence is evaluated in chunks of 64 tokens on the matrix cores with
  * float32 accumulation. For bfloat16 io the operands of y's two products that
@@ -25,11 +26,10 @@
  * parts, as two where the state is not returned). For float32 io each operand
  * is three bfloat16 parts, to float32 accuracy; there an infinity may make NaN
  * of the outputs and states that it enters, and what lies below 1e-38 in a
- * value is lost. The result equals the
- * recurrence up to rounding and is bitwise reproducible. A token's output
- * depends only on the tokens of its own document up to it: where others hold
- * infinities or NaN it has the bits that it has without them, and so have the
- * gradients.
+ * value is lost. The result equals the recurrence up to rounding and is bitwise
+ * reproducible. A token's output depends only on the tokens of its own document
+ * up to it: where others hold infinities or NaN it has the bits that it has
+ * without them, and so have the gradients.
  *
  * Layouts and limits of all calls:
  *   q, k         [batch][seqlen][ngroups][d_k] io, 16-byte aligned

@@ -994,7 +994,8 @@ __global__ __launch_bounds__(kThreads) void la_join_kernel(const LaArgs a) {
     const bool cut = SEQ && a.flags[(p.role * a.batch + p.b) * a.nseg + j - 1] != 0;
     const f4 own = *reinterpret_cast<const f4*>(w + j * step);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) s[r] = cut ? own[r] : fmaf(s[r], keep, own[r]);
+    for (int r = 0; r < 4; ++r)  // a state of 0 stays out: keep is infinite where a segment of a growing head is long
+      s[r] = cut || s[r] == 0.0f ? own[r] : fmaf(s[r], keep, own[r]);
     *reinterpret_cast<f4*>(w + j * step) = s;
   }
 }

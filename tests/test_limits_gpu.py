@@ -7,8 +7,9 @@ import torch
 
 import selective_state_space_07_amd as ms
 from oracle import gnorm as gn
+from oracle import linattn as la
 from tests.test_gnorm_gpu import DT, U
-from tests.test_linattn_gpu import BF, bwd_args, check_bwd, check_fwd, fwd_args, gpu, make, say
+from tests.test_linattn_gpu import BF, absolute, bwd_args, check_bwd, check_fwd, fwd_args, gpu, make, say, steps
 
 pytestmark = pytest.mark.gpu
 
@@ -101,3 +102,21 @@ def test_decays_above_zero(shape, dtype):
     torch.cuda.synchronize()
     check_fwd(a, got, "growing")
     check_bwd(a, grads, "growing")
+
+
+@pytest.mark.parametrize("L,decay", [(128, 1.3), (8192, 0.5)])
+def test_a_growing_head_that_starts_from_nothing(L, decay):
+    """Keys of 0 up to the last tokens: the power of lam over all that (lam^8192 is far beyond float32) has nothing to
+    multiply, in one segment and in several."""
+    a = make(1, L, 1, 1, 32, 32, torch.float32, seed=84)
+    a["k"][:, :-20] = 0
+    a["log_decay"] = torch.tensor([decay])
+    assert (ms.lin_attn_workspace_bytes(1, L, 1, 1, 32, 32, torch.float32) > 0) == (L > 1000)
+    d = gpu(a)
+    y, s = ms.lin_attn_fwd(*fwd_args(d))
+    torch.cuda.synchronize()
+    want, size = la.oracle_fwd(*fwd_args(a)), la.oracle_fwd(*fwd_args(absolute(a)))
+    # as many roundings as a sequence of the last two chunks has
+    tol = steps(dict(a, q=a["q"][:, -128:])) * U
+    for got, w, m in zip((y, s), want, size):
+        assert (np.abs(got.cpu().double().numpy() - w) <= tol * m + 1e-30).all()
