@@ -35,15 +35,24 @@
 // significant bits each, which hold a float32 whole, and a product takes its
 // six largest products of parts (the next are below 2^-23 of it).
 //
+// For bfloat16 io the scores and the state, float32 values that meet operands of
+// 8 significant bits, are two parts each: 16 bits, so that y has the error of its
+// own rounding alone, 1.66e-3 of itself in the mean. With one part each that was
+// 2.35e-3, at 58 us instead of 73 for 8 x 2048 tokens, 12 heads of 128, and 155
+// instead of 193 for the gradients.
+//
 // Measured on an MI355X, where a large copy reaches 5.2 TB/s: 8 x 2048 tokens,
-// 12 heads of 128, bfloat16: 57 us (201 MB to read and write, 3.5 TB/s; 209 us
-// with one task after the other, four barriers a chunk and bank conflicts), the
-// gradients 154 us (352 MB, 2.3 TB/s: 576 workgroups are two and a quarter
-// rounds of 256 CUs and take three). Both are bound by the stream of K, V, Q
-// and y: without any of the products they take 56 and 142 us, without that
-// traffic 45 and 130. Four chunks ahead instead of two changed nothing (58 and
-// 161 us). Two workgroups on a CU would need the kernel in 128 registers a
-// lane; there it spills (prompt 76 us).
+// 12 heads of 128, bfloat16: 73 us (201 MB to read and write, 2.8 TB/s), the
+// gradients 193 us (352 MB, 1.8 TB/s: 576 workgroups are two and a quarter
+// rounds of 256 CUs and take three). Both are bound by the issue of instructions
+// (of the 4900 cycles of a chunk the gradients' vector instructions take 1870 on
+// each SIMD and the matrix ones 1490): without the state's products they take 64
+// and 175 us, without y's 63 and 173, without either 58 and 162, without the
+// traffic of K, V, Q and y 64 and 181. With one part of scores and state each,
+// one task after the other, four barriers a chunk and bank conflicts took 209 us
+// instead of 58, and four chunks ahead instead of two changed nothing (58 and
+// 161 us). Two workgroups on a CU would need 80 KB of LDS each, not 116, and 128
+// registers a lane, not 170.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -84,10 +93,13 @@ struct Parts {
 // An operand of the io type: bfloat16 is one part, float32 three.
 template <int IO>
 using Op = Parts<IO == 1 ? 1 : 3>;
+// A float32 value that is multiplied with one: a score, or the state.
+template <int IO>
+using Sum = Parts<IO == 1 ? 2 : 3>;
 
 typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
-// Two values as one word of bfloat16, rounded, or (for the first of several
-// parts) cut: rounding would take finite values beyond 3.38e38 to infinity.
+// Two values as one word of bfloat16, rounded, or (as the first of several parts)
+// cut: rounding would take finite values beyond 3.38e38 to infinity.
 __device__ __forceinline__ uint32_t round2(float a, float b) {
   uint32_t w = __builtin_bit_cast(uint32_t, bf2{static_cast<__bf16>(a), static_cast<__bf16>(b)});
   asm("" : "+v"(w));  // or the compiler would round the two one by one, to unpack them from there
@@ -136,13 +148,14 @@ __device__ __forceinline__ Parts<N> split(f4 lo, f4 hi) {
   }
   return o;
 }
-// The same of four values, two to a word.
-template <int N>
+// The same of four values, two to a word; where none is beyond 3.38e38 the first
+// part may be rounded, which leaves the last of two a quarter of the error.
+template <bool CUT, int N>
 __device__ __forceinline__ void split4(f4 v, u2 (&o)[N]) {
   float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int p = 0; p < N; ++p) {
-    const bool cut = p == 0 && N > 1;
+    const bool cut = CUT && p == 0 && N > 1;
     const uint32_t a = cut ? cut2(x[0], x[1]) : round2(x[0], x[1]), b = cut ? cut2(x[2], x[3]) : round2(x[2], x[3]);
     o[p] = u2{a, b};
     rest2(x[0], x[1], a);
@@ -175,15 +188,22 @@ __device__ __forceinline__ Parts<N> between(const Parts<N>& f, int first, int la
               ((2 * j + 1 >= first) & (2 * j + 1 <= last) ? 0xFFFF0000u : 0u);
   return masked(f, mask);
 }
-// Those that are finite (of the others the first part is not).
+// Where they are finite: elsewhere the first part is not.
 template <int N>
-__device__ __forceinline__ Parts<N> finite(const Parts<N>& f) {
+__device__ __forceinline__ u4 finite(const Parts<N>& f) {
   const u4 w = __builtin_bit_cast(u4, f.p[0]);
   u4 mask;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     mask[j] = ((w[j] & 0x7F80u) != 0x7F80u ? 0xFFFFu : 0u) | ((w[j] & 0x7F800000u) != 0x7F800000u ? 0xFFFF0000u : 0u);
-  return masked(f, mask);
+  return mask;
+}
+// An infinity or NaN whole in its first part: the rests of it are NaN, and 0 here.
+template <int N>
+__device__ __forceinline__ Parts<N> whole(const Parts<N>& f) {
+  Parts<N> o = masked(f, finite(f));
+  o.p[0] = f.p[0];
+  return o;
 }
 // acc[i] += a[i] b over the pairs of parts that matter, the smallest first, and
 // each pair for all i in turn: consecutive products do not wait for each other.
@@ -204,15 +224,15 @@ __device__ __forceinline__ void mma_each(f4* acc, const Parts<NA> (&a)[M], const
 
 // The operand that two neighbouring tiles of accumulators are: 8 consecutive
 // rows, of which the first tile has the upper four where g is odd.
-template <int IO>
-__device__ __forceinline__ Op<IO> tiles_op(f4 even, f4 odd, int g) {
+template <int N>
+__device__ __forceinline__ Parts<N> tiles_op(f4 even, f4 odd, int g) {
   const bool up = g & 1;
-  if constexpr (IO == 1) {
+  if constexpr (N == 1) {
     const u4 v = __builtin_bit_cast(u4, frag_regs<1>(even, odd).v);
     const u4 w = {up ? v.z : v.x, up ? v.w : v.y, up ? v.x : v.z, up ? v.y : v.w};
-    return Op<1>{{__builtin_bit_cast(bf8, w)}};
+    return Parts<1>{{__builtin_bit_cast(bf8, w)}};
   } else {
-    return split<3>(up ? odd : even, up ? even : odd);
+    return split<N>(up ? odd : even, up ? even : odd);
   }
 }
 
@@ -271,11 +291,11 @@ struct Rows {
 // All reads are (base ^ constant) + constant with a base that depends on the
 // lane alone: a step along the row changes bits that the exchange leaves to
 // the exclusive-or, and 4 or 32 rows further the exchange is the same.
-// A float32 tile lies there as its three parts, each a bfloat16 tile.
-template <int IO, int W, int NT>
+// A tile of several parts lies there as that many bfloat16 tiles.
+template <int IO, int W, int NT, typename OP = Op<IO>>
 struct Tile {
   using T = typename Io<IO>::T;
-  static constexpr int kParts = IO == 1 ? 1 : 3;
+  static constexpr int kParts = sizeof(OP) / sizeof(bf8);
   static constexpr uint32_t kRow = W * 2, kPart = kC * kRow, kBytes = kParts * kPart;  // bytes in LDS
   static constexpr int kPer = W * sizeof(T) / 16;  // 16-byte pieces of a row in memory
   static constexpr int kN = kC * kPer / NT;        // pieces of a thread
@@ -318,14 +338,15 @@ struct Tile {
       if constexpr (IO == 1) {
         *reinterpret_cast<u4*>(p) = v[q];
       } else {
-        put4(p, __builtin_bit_cast(f4, v[q]));
+        put4<true>(p, __builtin_bit_cast(f4, v[q]));
       }
     }
   }
-  // Four neighbouring elements, rounded to bfloat16 or split into the parts.
+  // Four neighbouring elements, split into the parts.
+  template <bool CUT>
   static __device__ __forceinline__ void put4(char* p, f4 x) {
     u2 o[kParts];
-    split4(x, o);
+    split4<CUT>(x, o);
 #pragma unroll
     for (int i = 0; i < kParts; ++i) *reinterpret_cast<u2*>(p + i * kPart) = o[i];
   }
@@ -345,9 +366,9 @@ struct Tile {
 
   // Row-major operands, k-values 32 kb + 8 g .. of row spread(i, l15).
   static __device__ __forceinline__ uint32_t row_base(int l15, int g) { return at(spread(0, l15), 8 * g); }
-  static __device__ __forceinline__ Op<IO> row(const char* lds, uint32_t base, int i, int kb) {
+  static __device__ __forceinline__ OP row(const char* lds, uint32_t base, int i, int kb) {
     const char* p = lds + 32 * (i >> 1) * kRow + ((base ^ (4 * (i & 1) * kRow)) ^ (64 * kb));
-    Op<IO> f;
+    OP f;
 #pragma unroll
     for (int n = 0; n < kParts; ++n) f.p[n] = __builtin_bit_cast(bf8, *reinterpret_cast<const u4*>(p + n * kPart));
     return f;
@@ -361,11 +382,11 @@ struct Tile {
   }
   // What takes a column base from spread(0, .) to spread(i, .).
   static __device__ __forceinline__ uint32_t col_step(int i) { return (i >> 1) * 64 + (i & 1) * 8; }
-  static __device__ __forceinline__ Op<IO> col(const char* lds, uint32_t base, int i, int kb) {
+  static __device__ __forceinline__ OP col(const char* lds, uint32_t base, int i, int kb) {
     typedef short s4 __attribute__((ext_vector_type(4)));
     typedef __attribute__((address_space(3))) s4* lds_s4;
     const char* p = lds + 32 * kb * kRow + (base ^ col_step(i));
-    Op<IO> f;
+    OP f;
 #pragma unroll
     for (int n = 0; n < kParts; ++n) {
       const u2 lo = __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(p + n * kPart)));
@@ -440,8 +461,8 @@ struct Ids {
 __device__ __forceinline__ int last_of(uint64_t begins) { return begins ? 63 - __builtin_clzll(begins) : 0; }
 
 // S^T of one wave: column v0 + spread(wave, l15), k-elements spread(i, 4 g) + r.
-// Kernels and workspace hold half the state, which is exact, so that rounding to
-// bfloat16 takes no finite one to infinity.
+// Kernels and workspace hold half the state, which is exact, so that rounding its
+// first part to bfloat16 takes no finite one to infinity.
 constexpr float kHalf = 0.5f;
 template <int KD>
 struct State {
@@ -470,10 +491,11 @@ struct State {
   // S^T = lam^n S^T + K^T (w V) over the tokens of the last document; w_in
   // holds the tokens' weights, keep is lam^n.
   //
-  // The state is kept and returned in float32, so for bfloat16 io as well the
-  // products w v (24 significant bits) are three parts. Where the state is not
-  // returned, only y sees it, rounded to bfloat16 itself, and two parts (16
-  // bits) do; one would double the rounding that y gets.
+  // The state is kept in float32, so for bfloat16 io as well the products w v (24
+  // significant bits) are three parts. Two (`three` false) are left of them where
+  // the state is never returned, in the sums for dq and dk, which read it in two
+  // parts themselves (193 us instead of 201 for the gradients of 8 x 2048 tokens,
+  // 12 heads of 128).
   template <int IO, bool SEQ, typename TileK>
   __device__ __forceinline__ void add(const char* Ks, uint32_t at_col, const Op<IO> (&vf)[2], const float* w_in,
                                       float keep, uint64_t begins, int g, bool three) {
@@ -492,7 +514,7 @@ struct State {
         x[j] = get(vf[kb], j) * w[j >> 2][j & 3];
         if (SEQ) x[j] = 32 * kb + 8 * g + j >= last ? x[j] : 0.0f;
       }
-      const u4 first = pack<true>(x);
+      const u4 first = pack<false>(x);
       rest(x, first);
       if (IO == 1 && __any(unfit(first, 0.0f) != 0.0f)) {  // an infinity or NaN is whole in its first part: its rest is NaN
         asm volatile("");                                  // a branch, not selects
@@ -534,14 +556,14 @@ struct Plan {
   static constexpr int kThreadsY = 2 * kThreads;
   using TileK = Tile<IO, KD, kThreadsY>;
   using TileV = Tile<IO, kVS, kThreadsY>;
-  using TileS = Tile<IO, KD, kThreadsY>;  // [column of v][k-element]
+  using TileS = Tile<IO, KD, kThreadsY, Sum<IO>>;  // [column of v][k-element]
   static constexpr int kKV = TileK::kBytes + TileV::kBytes, kS = TileS::kBytes, kMost = 160 * 1024 - 1024;
   static constexpr int kTBuf = 2 * kKV + kS <= kMost ? 2 : 1, kSBuf = 2 * kKV + 2 * kS <= kMost ? 2 : 1;
   static_assert(kTBuf * kKV + kSBuf * kS <= kMost, "LDS");
   // Chunks that K, V and Q are ahead in registers: two, but one where two would
   // spill (float32 128 wide: 8 x 2048, 12 heads, 178 us, 198 with two) and where
   // two workgroups share a CU and its registers (bfloat16 64 wide: 8 x 2048, 24
-  // heads, packed: gradients 137 us, 145 with two; 50 and 49 us not packed).
+  // heads, packed: gradients 143 us, 174 with two; 130 and 129 us not packed).
   static constexpr int kAhead = (IO == 0) == (KD == 128) ? 1 : 2;
 };
 
@@ -553,7 +575,7 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
   using TileK = typename P::TileK;
   using TileV = typename P::TileV;
   using TileS = typename P::TileS;
-  constexpr int kKb = KD / 32, kTBuf = P::kTBuf, kSBuf = P::kSBuf, kAhead = P::kAhead;
+  constexpr int kKb = KD / 32, kSum = IO == 1 ? 2 : 3, kTBuf = P::kTBuf, kSBuf = P::kSBuf, kAhead = P::kAhead;
   constexpr uint32_t kBufK = 0, kBufV = kTBuf * TileK::kBytes, kBufS = kBufV + kTBuf * TileV::kBytes;
   __shared__ __attribute__((aligned(512))) char lds[kBufS + kSBuf * TileS::kBytes];
   // powers of lam with their factors: of a score at distance 63 - m (0 from 64
@@ -570,7 +592,7 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
   float sc_out = R.sc_out, sc_kv = R.sc_kv;
   void* out_p = R.out;
   int es_out = IO == 0 || R.out_f32 ? 4 : 2, off = R.off, rev_i = R.rev, nheads = a.nheads, seqlen = a.seqlen;
-  int three_i = __builtin_amdgcn_readfirstlane(R.state_out != nullptr);
+  int three_i = R.keeps;
   asm volatile("" : "+s"(sc_out), "+s"(sc_kv), "+s"(out_p), "+s"(es_out), "+s"(off), "+s"(rev_i), "+s"(nheads),
                "+s"(seqlen), "+s"(kd), "+s"(vd), "+s"(three_i));
   const bool rev = rev_i != 0, three = three_i != 0;
@@ -636,11 +658,10 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
   if (!makes_y) {
     const int col = v0 + spread(wv, l15);
     State<KD> S;
-    // writes this wave's columns of S to the chunk's tile, in the io type
-    // (rounded to bfloat16: the choice that makes y's products plain ones)
+    // writes this wave's columns of S to the chunk's tile
     auto put_state = [&](char* to) {
 #pragma unroll
-      for (int i = 0; i < State<KD>::kTiles; ++i) TileS::put4(to + TileS::at(spread(wv, l15), spread(i, 4 * g)), S.t[i]);
+      for (int i = 0; i < State<KD>::kTiles; ++i) TileS::template put4<false>(to + TileS::at(spread(wv, l15), spread(i, 4 * g)), S.t[i]);
     };
     start();
     S.zero();
@@ -771,25 +792,33 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
             sc[i][r] = !SEQ || s + r >= from ? sc[i][r] * wt[r] : 0.0f;
         }
       }
-      auto carried = [&](uint32_t at) {
+      // rows of S's tiles at a time: four would spill in 128 registers (8 x 2048,
+      // 24 heads of 64, packed: gradients 150 us with four, 147 with two)
+      constexpr int kG = IO == 1 && KD == 64 ? 2 : 4;
+      auto carried = [&](uint32_t at, auto again) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int kb = 0; kb < kKb; ++kb) {
-          Op<IO> sf[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sf[i] = TileS::row(Ss, at, i, kb);
-          mma_each(y, sf, qf[kb]);
+          for (int i0 = 0; i0 < 4; i0 += kG) {
+            Sum<IO> sf[kG];
+#pragma unroll
+            for (int i = 0; i < kG; ++i) {
+              sf[i] = TileS::row(Ss, at, i0 + i, kb);
+              if (again.value) sf[i] = whole(sf[i]);
+            }
+            mma_each(y + i0, sf, qf[kb]);
+          }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int r = 0; r < 4; ++r) y[i][r] = open ? y[i][r] * w_out : 0.0f;
       };
-      carried(at_row);
-      // the scores are rounded to the io type here, once
-      const Op<IO> s0 = tiles_op<IO>(sc[0], sc[1], gg), s1 = tiles_op<IO>(sc[2], sc[3], gg);
-      auto weighted = [&](const Op<IO>& p, int kb) {
+      carried(at_row, std::false_type{});
+      const Sum<IO> s0 = tiles_op<kSum>(sc[0], sc[1], gg), s1 = tiles_op<kSum>(sc[2], sc[3], gg);
+      auto weighted = [&](const Sum<IO>& p, int kb) {
         Op<IO> vf[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) vf[i] = TileV::col(Vs, at_v, i, kb);
@@ -804,34 +833,37 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
         for (int r = 0; r < 4; ++r) bad = fmaf(y[i][r], 0.0f, bad);
       // An infinity or NaN in k or v also reaches the tokens that it is masked
       // for, as 0 * inf. Where any sum is not finite the sums are taken again, in
-      // the same order, with 0 for masked scores and for values that are not
-      // finite; the latter are added behind, where they are not masked. So a sum
-      // that none of them belongs to has the bits that it has without them.
+      // the same order, with 0 for masked scores, for values that are not finite
+      // and for the rests of scores and states that are not; the values are added
+      // behind, where they are not masked. So a sum that none of them belongs to
+      // has the bits that it has without them.
       if (__any(bad != 0.0f)) {
         uint32_t again = row_b, again_v = col_v;
         asm volatile("" : "+v"(again), "+v"(again_v));  // read again, not kept from above
-        carried(again);
-        const Op<IO> p0 = between(s0, from - 8 * gg, t - 8 * gg), p1 = between(s1, from - 8 * gg - 32, t - 8 * gg - 32);
+        carried(again, std::true_type{});
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
+        for (int kb = 0; kb < 2; ++kb) {
+          const int o = 32 * kb + 8 * gg;  // token of the lane's first score
+          const Sum<IO> p = whole(between(kb == 0 ? s0 : s1, from - o, t - o));
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const Op<IO> vf[1] = {finite(TileV::col(Vs, again_v, i, kb))};
-            mma_each(y + i, vf, kb == 0 ? p0 : p1);
+            const Op<IO> v = TileV::col(Vs, again_v, i, kb), vf[1] = {masked(v, finite(v))};
+            mma_each(y + i, vf, p);
           }
 #pragma unroll 1
-        for (int gs = 0; gs < 4; ++gs) {
+          for (int gs = 0; gs < 4; ++gs) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const int s = 32 * (k >> 3) + 8 * gs + (k & 7);
-            const float p = __shfl(k < 8 ? get(p0, k & 7) : get(p1, k & 7), 16 * gs + l15, 64);
-            if (s > t || s < from) continue;
+            for (int j = 0; j < 8; ++j) {
+              const int s = 32 * kb + 8 * gs + j;
+              const float w = __shfl(get(p, j), 16 * gs + l15, 64);
+              if (s > t || s < from) continue;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const f4 v = TileV::get4(Vs, s, spread(i, 4 * gg));
+              for (int i = 0; i < 4; ++i) {
+                const f4 v = TileV::get4(Vs, s, spread(i, 4 * gg));
 #pragma unroll
-              for (int r = 0; r < 4; ++r)
-                if (v[r] * 0.0f != 0.0f) y[i][r] = fmaf(p, v[r], y[i][r]);
+                for (int r = 0; r < 4; ++r)
+                  if (v[r] * 0.0f != 0.0f) y[i][r] = fmaf(w, v[r], y[i][r]);
+              }
             }
           }
         }
@@ -887,7 +919,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 
   const int64_t first = static_cast<int64_t>(pl.b) * seqlen + (rev ? seqlen - 1 : 0);
   const Rows kr = rows_of<T>(R.k, pl, rep, kd, 0, KD, first, rev);
   const Rows vr = rows_of<T>(R.v, pl, rep, vd, v0, kVS, first, rev);
-  const bool three = __builtin_amdgcn_readfirstlane(R.state_out != nullptr) != 0;
+  const bool three = R.keeps;
   // Only the segment's last document adds to its state: the sum starts in the
   // chunk where that begins, found from the segment's end, 1024 tokens at a time
   // (2 x 4133, 24 heads of 64 x 96, float32: 30 us for all sums, 44 in full).
@@ -1028,17 +1060,22 @@ size_t state_floats(const LaPlan& p, int32_t batch, int32_t nheads, int32_t kd, 
 
 }  // namespace
 
-// One workgroup per CU is resident, so the sums of a call run in rounds of 32
-// workgroups on each XCD, and segments fill the rounds where sequences are few.
+// The estimate counts one workgroup on a CU: the sums of a call run in rounds of
+// 32 workgroups on each XCD, and segments fill the rounds where sequences are
+// few. (Of bfloat16 heads of up to 64 two fit, which hide one another's waits
+// rather than halve the time. Counted as two, without the second parts of scores
+// and state: 8 x 2048, 24 heads, 65 us instead of 43, the gradients of 4 x 4096,
+// 16 heads, 90 instead of 75; only 1 x 65536, 12 heads, gained, 135 instead of
+// 145.)
 // Splitting reads k and v once more: the number of segments with the least
 // estimated time is taken, in chunks of one workgroup. A workgroup costs two
 // beside its own, a chunk of the segment sums 0.6 (they are as long as the
 // segment, or as all of them take at the rate of a CU), the join 2 and an eighth
 // for each segment. Measured: 8 x 2048, 12 heads of 128, bf16, 192 workgroups,
-// 58 us in one segment, 92 in four; 1 x 65536, 24 workgroups, 321 us in 21
-// segments (313 on another day), 322 in 32, 336 in 10; 2 x 4133, 24 heads of 64
-// x 96, float32, packed, 96 workgroups, 134 us in 5, 152 in 8, 133 in 2 (144,
-// 155 and 180 while the sums read whole segments, as without documents).
+// 73 us in one segment, 106 in four; 1 x 65536, 24 workgroups, 355 us in 21
+// segments, 358 in 32, 368 in 10; 2 x 4133, 24 heads of 64 x 96, float32, packed,
+// 96 workgroups, 131 us in 5, 148 in 8, 130 in 2 (144, 155 and 180 while the sums
+// read whole segments, as without documents).
 LaPlan la_plan(int32_t batch, int32_t seqlen, int32_t nheads, int32_t ngroups, int32_t d_k, int32_t d_v, int32_t nroles) {
   const int32_t nchunks = (seqlen + kC - 1) / kC;
   const int64_t units = static_cast<int64_t>(batch) * ngroups;

@@ -154,7 +154,7 @@ int mamba_linattn_fwd(int32_t batch, int32_t seqlen, int32_t nheads, int32_t ngr
   mscan::LaCall c{batch, seqlen, nheads, ngroups, io_dtype, seq_idx, log_decay, 1, {},
                   static_cast<float*>(workspace), static_cast<hipStream_t>(stream)};
   c.role[0] = mscan::LaRole{{q, q_stride, true}, {k, k_stride, true}, {v, v_stride, false}, d_k, d_v, y, false,
-                            state_in, false, state_out, scale, 1.0f, false, 1};
+                            state_in, false, state_out, scale, 1.0f, false, 1, true};
   return launched(mscan::launch_la(c, plan_fwd(d)));
 }
 
@@ -203,9 +203,9 @@ int mamba_linattn_bwd(int32_t batch, int32_t seqlen, int32_t nheads, int32_t ngr
   void* dk_to = shared ? ws + w.dk : dk;
   mscan::LaCall c{batch, seqlen, nheads, ngroups, io_dtype, seq_idx, log_decay, 3, {}, ws, s};
   const mscan::LaOperand oq{q, q_stride, true}, ok_{k, k_stride, true}, ov{v, v_stride, false}, ody{dy, dy_stride, false};
-  c.role[0] = mscan::LaRole{ody, ov, ok_, d_v, d_k, dq_to, shared, state_in, true, nullptr, scale, 1.0f, false, 1};
-  c.role[1] = mscan::LaRole{ov, ody, oq, d_v, d_k, dk_to, shared, dstate_out, true, nullptr, 1.0f, scale, true, 0};
-  c.role[2] = mscan::LaRole{ok_, oq, ody, d_k, d_v, dv, false, dstate_out, false, dstate_in, 1.0f, scale, true, 0};
+  c.role[0] = mscan::LaRole{ody, ov, ok_, d_v, d_k, dq_to, shared, state_in, true, nullptr, scale, 1.0f, false, 1, false};
+  c.role[1] = mscan::LaRole{ov, ody, oq, d_v, d_k, dk_to, shared, dstate_out, true, nullptr, 1.0f, scale, true, 0, false};
+  c.role[2] = mscan::LaRole{ok_, oq, ody, d_k, d_v, dv, false, dstate_out, false, dstate_in, 1.0f, scale, true, 0, true};
   hipError_t err = mscan::launch_la(c, plan_bwd(d));
   if (err == hipSuccess && shared)
     err = mscan::launch_la_head_sum(static_cast<int64_t>(rows), nheads, ngroups, d_k, io_dtype, ws + w.dq, dq, s);

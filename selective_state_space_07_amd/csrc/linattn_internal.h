@@ -30,6 +30,7 @@ struct LaRole {
   float sc_out, sc_kv;     // factors on what is read out, and on what enters the state
   bool rev;                // from the last token to the first
   int32_t off;             // 1: the incoming state stands one step before the first token; 0: at it
+  bool keeps;              // a role whose state may be returned, whether this call wants it or not
 };
 
 struct LaCall {
