@@ -27,7 +27,7 @@
 // Measured on an MI355X, where a large copy reaches 5.2 TB/s: 16384 x 1536
 // bfloat16, 12 groups, gate behind: 30 us (151 MB, 5.0 TB/s; 64 us with the gate
 // chosen at each element and one row at a time). Gradients of one group, RMS,
-// gate first: 59 us (252 MB, 4.3 TB/s: the sums meet twice a row, and what is
+// gate first: 60 us (252 MB, 4.2 TB/s: the sums meet twice a row, and what is
 // resident waits for them; 132 us with a wave to a row).
 #include "gnorm_internal.h"
 #include "mfma_frag.h"
@@ -634,11 +634,13 @@ Layout layout(int32_t channels, int32_t groups, int32_t io_dtype, bool can_vec, 
 }
 
 // Workgroups that share the rows of a tile, with as many turns for each. The
-// backward takes one round of what is resident, so that few partial sums are
-// left: by its registers 16 waves on a CU (float32: 24), or three workgroups
-// of four waves where a wave holds whole groups (16384 x 1536 bf16, one group,
-// three waves: 1280 workgroups 60 us, 1536 71 us, 768 69 us; twelve groups:
-// 768 workgroups 53 us, 1280 56 us).
+// backward takes about one round of what is resident, so that few partial sums
+// are left: 16 waves on a CU (float32: 24), or three workgroups of four waves
+// where a wave holds whole groups (16384 x 1536 bf16, one group, three waves:
+// 1280 workgroups 60 us, 1536 71 us, 768 69 us). Three are a round and a half
+// for the gate-first form, of which 181 registers let two be resident, and the
+// best for it all the same (twelve groups, bf16, two, three and four a CU: gate
+// first 68, 56 and 60 us, gate behind 54, 47 and 50, none 48, 39 and 41).
 int64_t blocks(const Layout& l, int64_t rows, int32_t io_dtype, bool bwd) {
   const int64_t per = l.wide ? 1 : static_cast<int64_t>(kWaves) * l.u * l.rp;
   const int64_t all = (rows + per - 1) / per;

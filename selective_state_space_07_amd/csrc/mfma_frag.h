@@ -1,6 +1,7 @@
 // Operands of the matrix cores as the SSD kernels use them (the linear-attention
-// kernels take the vector types and the rounded form): 8 consecutive k-values per lane, multiplied as one 16x16x32 bfloat16
-// step or as eight 16x16x4 float32 steps over the same 8 values.
+// kernels take the vector types and the rounded form): 8 consecutive k-values
+// per lane, multiplied as one 16x16x32 bfloat16 step or as eight 16x16x4 float32
+// steps over the same 8 values.
 #pragma once
 
 #include <hip/hip_runtime.h>
