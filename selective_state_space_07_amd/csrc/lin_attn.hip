@@ -1018,7 +1018,7 @@ __global__ __launch_bounds__(kThreads) void la_join_kernel(const LaArgs a) {
     }
     s *= kHalf;
   }
-  const float keep = power(a.log_decay[p.h] * kLog2e, a.seg_chunks * kC);
+  const float g2 = a.log_decay[p.h] * kLog2e, keep = power(g2, a.seg_chunks * kC);
   float* w = a.ws + ws_base<KD>(a, p, 0) + (i * kThreads + tid) * 4;
   const int64_t step = static_cast<int64_t>(a.nsl) * KD * kVS;
   *reinterpret_cast<f4*>(w) = s;
@@ -1026,8 +1026,12 @@ __global__ __launch_bounds__(kThreads) void la_join_kernel(const LaArgs a) {
     const bool cut = SEQ && a.flags[(p.role * a.batch + p.b) * a.nseg + j - 1] != 0;
     const f4 own = *reinterpret_cast<const f4*>(w + j * step);
 #pragma unroll
-    for (int r = 0; r < 4; ++r)  // a state of 0 stays out: keep is infinite where a segment of a growing head is long
-      s[r] = cut || s[r] == 0.0f ? own[r] : fmaf(s[r], keep, own[r]);
+    for (int r = 0; r < 4; ++r) {
+      // over a long segment keep is 0 or infinite where lam is neither: a state of
+      // 0 stays 0, and an infinite one infinite
+      const bool as_is = s[r] == 0.0f || (__builtin_isinf(s[r]) && g2 > -HUGE_VALF);
+      s[r] = cut ? own[r] : as_is ? s[r] + own[r] : fmaf(s[r], keep, own[r]);
+    }
     *reinterpret_cast<f4*>(w + j * step) = s;
   }
 }

@@ -120,3 +120,30 @@ def test_a_growing_head_that_starts_from_nothing(L, decay):
     tol = steps(dict(a, q=a["q"][:, -128:])) * U
     for got, w, m in zip((y, s), want, size):
         assert (np.abs(got.cpu().double().numpy() - w) <= tol * m + 1e-30).all()
+
+
+@pytest.mark.parametrize("where", ["v", "state"])
+@pytest.mark.parametrize("L", [300, 4200])
+def test_an_infinity_lasts(L, where):
+    """An infinite value or state is infinite at the end of a sequence, in one segment as in several, over which the
+    power of lam is below float32; a head without memory has 0 times it, NaN, at the next token already."""
+    a = make(1, L, 2, 2, 64, 64, torch.bfloat16, seed=85, state=True)
+    assert (ms.lin_attn_workspace_bytes(1, L, 2, 2, 64, 64, torch.bfloat16) > 0) == (L > 1000)
+    a["q"], a["k"] = a["q"].abs() + 0.5, a["k"].abs() + 0.5
+    a["log_decay"] = torch.tensor([-0.5, -0.01])
+    d = gpu(a)
+    y0, s0 = ms.lin_attn_fwd(*fwd_args(d))
+    bad = -float("inf")
+    if where == "v":
+        d["v"] = d["v"].clone()
+        d["v"][0, 5, :, 9] = bad
+    else:
+        d["state"] = d["state"].clone()
+        d["state"][0, :, 9] = bad
+    y, s = ms.lin_attn_fwd(*fwd_args(d))
+    torch.cuda.synchronize()
+    first = 5 if where == "v" else 0
+    assert (y[0, first:, :, 9] == bad).all() and (s[0, :, 9] == bad).all()
+    rest = torch.arange(64) != 9
+    assert torch.equal(y[..., rest], y0[..., rest]) and torch.equal(s[:, :, rest], s0[:, :, rest])
+    assert torch.equal(y[:, :first], y0[:, :first])
