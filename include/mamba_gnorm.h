@@ -21,8 +21,9 @@
  * mamba2_ssd_fwd.
  *
  * Statistics, sums and gradients of the parameters are float32 throughout
- * (the mean first, then the squares of the differences); outputs are rounded
- * to the io type once. Results are bitwise reproducible run to run.
+ * (the mean first, then the squares of the differences; values whose squares
+ * leave float32 are taken times a power of two); outputs are rounded to the io
+ * type once. Results are bitwise reproducible run to run.
  *
  * Layouts and limits:
  *   x, z, dy         [rows][channels] io, rows *_stride elements apart (at least

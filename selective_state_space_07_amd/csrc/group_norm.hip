@@ -173,6 +173,11 @@ __device__ __forceinline__ float reciprocal_root(float v) {
   return low ? r * 0x1p32f : r;
 }
 
+// Values whose squares, or whose sum, leave float32 (a sum of squares from 2^120
+// on, or NaN) are taken times 2^-80, exactly, and their statistics again. Where
+// these are 0 then, all values are equal, and 1 / sqrt(eps) is not scaled.
+constexpr float kLarge = 0x1p120f, kLess = 0x1p-80f;
+
 // sigmoid(z) = 1 / (1 + e), e = e^-z, and 1 - sigmoid(z) = e / (1 + e), the
 // latter without cancellation. Where e overflows the first is 0 and the minimum
 // takes the second from infinity times 0 to 1 (a NaN is in the first).
@@ -205,8 +210,10 @@ __device__ __forceinline__ float act_grad(int kind, float z, float& a) {
 
 // V elements a piece, K pieces a lane, U rows at a time. WIDE: one group of
 // one row per workgroup. GATE: one of the three, or kGateAny where the call says.
+// The gradients of eight pieces are held to the registers of three waves a SIMD
+// (16384 x 1500 bf16, five groups, gate first: 147 us, 267 us with two).
 template <int IO, int V, int K, int U, bool WIDE, bool BWD, int GATE>
-__global__ __launch_bounds__(WIDE ? 1024 : 64 * kWaves) void gnorm_kernel(const GnArgs a) {
+__global__ __launch_bounds__(WIDE ? 1024 : 64 * kWaves) __attribute__((amdgpu_waves_per_eu(K == 8 && BWD ? 3 : 1))) void gnorm_kernel(const GnArgs a) {
   using T = typename Io<IO>::T;
   const int gate_kind = GATE == kGateAny ? a.gate : GATE;
   static_assert(!WIDE || U == 1, "a workgroup's sums meet row by row");
@@ -272,7 +279,7 @@ __global__ __launch_bounds__(WIDE ? 1024 : 64 * kWaves) void gnorm_kernel(const 
   };
   for (; row0 < a.rows; row0 += per * a.nblk) {
     load(row0);
-    float x[U][K][V], z[U][K][V], d[BWD ? U : 1][K][V], gate[BWD ? U : 1][K][V], u[U][K][V], r[U];
+    float x[U][K][V], z[U][K][V], d[BWD ? U : 1][K][V], gate[BWD ? U : 1][K][V], u[U][K][V], r[U], rdx[U];
 #pragma unroll
     for (int q = 0; q < U; ++q)
 #pragma unroll
@@ -302,22 +309,48 @@ __global__ __launch_bounds__(WIDE ? 1024 : 64 * kWaves) void gnorm_kernel(const 
           }
           s += u[q][p][i];
         }
-      if (a.center) {
-        // divided, not multiplied by a rounded reciprocal: a group of equal values keeps no residue to be blown up
-        const float mu = sum1(s) / static_cast<float>(a.gs);
+      auto statistics = [&]() {  // of u, whose sum is s: its mean taken off, the sum of its squares
+        if (a.center) {
+          // divided, not multiplied by a rounded reciprocal: a group of equal values keeps no residue to be blown up
+          const float mu = sum1(s) / static_cast<float>(a.gs);
+#pragma unroll
+          for (int p = 0; p < K; ++p)
+#pragma unroll
+            for (int i = 0; i < V; ++i) u[q][p][i] = in_group[p] ? u[q][p][i] - mu : 0.0f;
+        }
+        s = 0.0f;
 #pragma unroll
         for (int p = 0; p < K; ++p)
 #pragma unroll
-          for (int i = 0; i < V; ++i) u[q][p][i] = in_group[p] ? u[q][p][i] - mu : 0.0f;
+          for (int i = 0; i < V; ++i) s = fmaf(u[q][p][i], u[q][p][i], s);
+        s = sum1(s);
+      };
+      statistics();
+      float scale = s < kLarge ? 1.0f : kLess;
+      if (__any(scale != 1.0f)) {  // the same for all of a workgroup that shares a group
+        s = 0.0f;
+#pragma unroll
+        for (int p = 0; p < K; ++p)
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            u[q][p][i] = x[q][p][i] * scale;
+            if (gate_kind == kGateFirst) u[q][p][i] *= BWD ? gate[q][p][i] : act(a.activation, z[q][p][i]);
+            s += u[q][p][i];
+          }
+        statistics();
+        if (s == 0.0f) scale = 1.0f;
+        if (BWD && gate_kind == kGateFirst)  // these are what dx and dz take of it
+#pragma unroll
+          for (int p = 0; p < K; ++p)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              x[q][p][i] *= scale;
+              gate[q][p][i] *= scale;
+            }
       }
-      s = 0.0f;
-#pragma unroll
-      for (int p = 0; p < K; ++p)
-#pragma unroll
-        for (int i = 0; i < V; ++i) s = fmaf(u[q][p][i], u[q][p][i], s);
       // 0 for the rows behind the last: with eps 0 their zeros would become NaN in the parameters' sums
-      s = sum1(s);
-      r[q] = row0 + q * rp + sub < a.rows ? reciprocal_root(fmaf(s, inv, a.eps)) : 0.0f;
+      r[q] = row0 + q * rp + sub < a.rows ? reciprocal_root(fmaf(s, inv, a.eps * scale * scale)) : 0.0f;
+      rdx[q] = gate_kind == kGateFirst ? r[q] : r[q] * scale;
     }
 
 #pragma unroll
@@ -369,7 +402,7 @@ __global__ __launch_bounds__(WIDE ? 1024 : 64 * kWaves) void gnorm_kernel(const 
         float dx[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          dx[i] = r[q] * (d[q][p][i] - m1 - u[q][p][i] * m2);
+          dx[i] = rdx[q] * (d[q][p][i] - m1 - u[q][p][i] * m2);
           if (gate_kind == kGateFirst) {
             z[q][p][i] *= dx[i] * x[q][p][i];
             dx[i] *= gate[q][p][i];
@@ -465,31 +498,37 @@ __global__ __launch_bounds__(1024) void gnorm_large_kernel(const GnArgs a) {
   for (int64_t row = blk; row < a.rows; row += a.nblk) {
     const int64_t at_x = row * a.x_row + ch0, at_z = row * a.z_row + ch0, at_dy = row * a.dy_row + ch0;
     const int64_t out = row * a.channels + ch0;
+    float scale = 1.0f;
     // the values of a piece before their norm (gated, where the gate is first)
     auto read = [&](int e, float (&x)[V], float (&z)[V], float (&u)[V]) {
       unpack<IO, V>(fetch<IO, V>(a.x, at_x + e, true), x);
       if (a.gate != kGateNone) unpack<IO, V>(fetch<IO, V>(a.z, at_z + e, true), z);
 #pragma unroll
-      for (int i = 0; i < V; ++i) u[i] = a.gate == kGateFirst ? x[i] * act(a.activation, z[i]) : x[i];
+      for (int i = 0; i < V; ++i) u[i] = scale * (a.gate == kGateFirst ? x[i] * act(a.activation, z[i]) : x[i]);
     };
     float x[V], z[V], u[V], v[2], mu = 0.0f, t = 0.0f;
-    if (a.center) {
+    for (int turn = 0; turn < 2; ++turn) {
+      if (a.center) {
+        t = 0.0f;
+        pieces([&](int, int e) {
+          read(e, x, z, u);
+#pragma unroll
+          for (int i = 0; i < V; ++i) t += u[i];
+        });
+        sum(t, 0.0f, v);
+        mu = v[0] / static_cast<float>(a.gs);  // divided: see above
+      }
+      t = 0.0f;
       pieces([&](int, int e) {
         read(e, x, z, u);
 #pragma unroll
-        for (int i = 0; i < V; ++i) t += u[i];
+        for (int i = 0; i < V; ++i) t = fmaf(u[i] - mu, u[i] - mu, t);
       });
       sum(t, 0.0f, v);
-      mu = v[0] / static_cast<float>(a.gs);  // divided: see above
+      if (v[0] < kLarge) break;  // the same for all threads
+      scale = kLess;
     }
-    t = 0.0f;
-    pieces([&](int, int e) {
-      read(e, x, z, u);
-#pragma unroll
-      for (int i = 0; i < V; ++i) t = fmaf(u[i] - mu, u[i] - mu, t);
-    });
-    sum(t, 0.0f, v);
-    const float r = reciprocal_root(fmaf(v[0], inv, a.eps));
+    const float less = v[0] == 0.0f ? 1.0f : scale, r = reciprocal_root(fmaf(v[0], inv, a.eps * less * less));
     float w[V], b[V];
     if constexpr (!BWD) {
       pieces([&](int, int e) {
@@ -544,9 +583,10 @@ __global__ __launch_bounds__(1024) void gnorm_large_kernel(const GnArgs a) {
           d[i] = r * (d[i] * w[i] - m0 - u[i] * m1);
           if (a.gate == kGateFirst) {
             float g;
-            z[i] = act_grad(a.activation, z[i], g) * d[i] * x[i];
+            z[i] = act_grad(a.activation, z[i], g) * d[i] * (x[i] * less);
             d[i] *= g;
           }
+          d[i] *= less;
         }
         put<IO, V>(static_cast<T*>(a.out) + out + e, d);
         if (a.gate != kGateNone) put<IO, V>(static_cast<T*>(a.dz) + out + e, z);
