@@ -165,18 +165,13 @@ __device__ __forceinline__ void wide_sum(float (&v)[N], float (&red)[2][N][16], 
   }
 }
 
-// 1 / sqrt(v). The instruction takes what lies below 2^-126 for 0, and with an
-// eps of 0 the mean square of values around 1e-20 does.
-__device__ __forceinline__ float reciprocal_root(float v) {
-  const bool low = v < 0x1p-100f;
-  const float r = __builtin_amdgcn_rsqf(low ? v * 0x1p64f : v);
-  return low ? r * 0x1p32f : r;
+// Values whose squares, or whose sum, leave float32 at its upper end (a sum of
+// squares from 2^120 on, or NaN) are taken times 2^-80, exactly, and their
+// statistics again; at its lower end (without an eps) times 2^90. Where these
+// are 0 then, all values are equal, and 1 / sqrt(eps) is not scaled.
+__device__ __forceinline__ float scale_for(float squares, float mean_square) {
+  return !(squares < 0x1p120f) ? 0x1p-80f : mean_square < 0x1p-100f ? 0x1p90f : 1.0f;
 }
-
-// Values whose squares, or whose sum, leave float32 (a sum of squares from 2^120
-// on, or NaN) are taken times 2^-80, exactly, and their statistics again. Where
-// these are 0 then, all values are equal, and 1 / sqrt(eps) is not scaled.
-constexpr float kLarge = 0x1p120f, kLess = 0x1p-80f;
 
 // sigmoid(z) = 1 / (1 + e), e = e^-z, and 1 - sigmoid(z) = e / (1 + e), the
 // latter without cancellation. Where e overflows the first is 0 and the minimum
@@ -326,7 +321,7 @@ __global__ __launch_bounds__(WIDE ? 1024 : 64 * kWaves) __attribute__((amdgpu_wa
         s = sum1(s);
       };
       statistics();
-      float scale = s < kLarge ? 1.0f : kLess;
+      float scale = scale_for(s, fmaf(s, inv, a.eps));
       if (__any(scale != 1.0f)) {  // the same for all of a workgroup that shares a group
         s = 0.0f;
 #pragma unroll
@@ -349,7 +344,7 @@ __global__ __launch_bounds__(WIDE ? 1024 : 64 * kWaves) __attribute__((amdgpu_wa
             }
       }
       // 0 for the rows behind the last: with eps 0 their zeros would become NaN in the parameters' sums
-      r[q] = row0 + q * rp + sub < a.rows ? reciprocal_root(fmaf(s, inv, a.eps * scale * scale)) : 0.0f;
+      r[q] = row0 + q * rp + sub < a.rows ? __builtin_amdgcn_rsqf(fmaf(s, inv, a.eps * scale * scale)) : 0.0f;
       rdx[q] = gate_kind == kGateFirst ? r[q] : r[q] * scale;
     }
 
@@ -525,10 +520,10 @@ __global__ __launch_bounds__(1024) void gnorm_large_kernel(const GnArgs a) {
         for (int i = 0; i < V; ++i) t = fmaf(u[i] - mu, u[i] - mu, t);
       });
       sum(t, 0.0f, v);
-      if (v[0] < kLarge) break;  // the same for all threads
-      scale = kLess;
+      if (turn == 0) scale = scale_for(v[0], fmaf(v[0], inv, a.eps));  // the same for all threads
+      if (scale == 1.0f) break;
     }
-    const float less = v[0] == 0.0f ? 1.0f : scale, r = reciprocal_root(fmaf(v[0], inv, a.eps * less * less));
+    const float less = v[0] == 0.0f ? 1.0f : scale, r = __builtin_amdgcn_rsqf(fmaf(v[0], inv, a.eps * less * less));
     float w[V], b[V];
     if constexpr (!BWD) {
       pieces([&](int, int e) {

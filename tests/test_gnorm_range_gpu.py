@@ -50,6 +50,34 @@ def test_large_values(power, shape, dtype, gate):
             torch.testing.assert_close(g[n], gb[n] + go[n], rtol=16 * U, atol=64 * U * float(g[n].abs().max()))
 
 
+@pytest.mark.parametrize("gate", ["none", "after", "first"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("power", [-60, -74, -100])
+def test_small_values_without_eps(power, shape, dtype, gate):
+    """Values whose squares lose bits, or vanish, beside ordinary ones and a row of zeros (0 / 0)."""
+    c, groups = shape
+    say("small", power, shape, dtype, gate)
+    a = make(9, c, groups, DT[dtype], gate, seed=93)
+    little = torch.ones(9, 1)
+    little[[1, 4, 5, 8]] = 2.0 ** power
+    small = little[:, 0] < 1
+    for center in (True, False):
+        kw = dict(gate_first=gate == "first", center=center, eps=0.0)
+        d, e = gpu(a), gpu(dict(a, x=(a["x"].float() * little).to(DT[dtype])))
+        y, g = fwd(e, **kw), bwd(e, **kw)
+        y0, g0 = fwd(d, **kw), bwd(d, **kw)
+        e["x"][2] = 0
+        y2 = fwd(e, **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(y, y0) and torch.isfinite(y).all()
+        assert torch.equal(g["dx"][small].double() * 2.0 ** power, g0["dx"][small].double())
+        assert torch.equal(g["dx"][~small], g0["dx"][~small])
+        for n in ("dweight", "dbias", "dz"):
+            assert n not in g or torch.equal(g[n], g0[n]), n
+        assert torch.isnan(y2[2]).all() and torch.equal(y2[3:], y[3:])
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
 def test_rows_at_the_ends_of_the_type(shape, dtype):
