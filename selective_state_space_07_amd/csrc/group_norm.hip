@@ -205,10 +205,10 @@ __device__ __forceinline__ float act_grad(int kind, float z, float& a) {
 
 // V elements a piece, K pieces a lane, U rows at a time. WIDE: one group of
 // one row per workgroup. GATE: one of the three, or kGateAny where the call says.
-// The gradients of eight pieces are held to the registers of three waves a SIMD
-// (16384 x 1500 bf16, five groups, gate first: 147 us, 267 us with two).
+// With that the gradients of eight pieces spill, or leave a SIMD two waves (16384
+// x 1500 bf16, five groups, gate first: 267 us, 127 us with the gate compiled in).
 template <int IO, int V, int K, int U, bool WIDE, bool BWD, int GATE>
-__global__ __launch_bounds__(WIDE ? 1024 : 64 * kWaves) __attribute__((amdgpu_waves_per_eu(K == 8 && BWD ? 3 : 1))) void gnorm_kernel(const GnArgs a) {
+__global__ __launch_bounds__(WIDE ? 1024 : 64 * kWaves) void gnorm_kernel(const GnArgs a) {
   using T = typename Io<IO>::T;
   const int gate_kind = GATE == kGateAny ? a.gate : GATE;
   static_assert(!WIDE || U == 1, "a workgroup's sums meet row by row");
@@ -721,7 +721,7 @@ hipError_t launch_io(const GnCall& c, const Layout& l, const GnArgs& a) {
     return l.k == 1 ? launch_typed<IO, V, 1, 1, 1, true>(c, l, a) : launch_large<IO, V>(c, l, a);
   }
   if (l.vec == 1)
-    return l.k == 2 ? launch_typed<IO, 1, 2, 1, 1, false>(c, l, a) : launch_gate<IO, 1, 8, 1, 1, false, kGateAny>(c, l, a);
+    return l.k == 2 ? launch_typed<IO, 1, 2, 1, 1, false>(c, l, a) : launch_typed<IO, 1, 8, 1, 1, false>(c, l, a);
   return launch_typed<IO, V, 1, 4, 2, false>(c, l, a);
 }
 
