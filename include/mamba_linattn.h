@@ -24,13 +24,14 @@
  * are not inputs (the decayed scores q.k, and S) are two bfloat16 parts each, 16
  * bits, so that outputs have the error of their own rounding; the state itself
  * is summed in float32 (w v enters its products as three parts). For float32 io
- * each operand is three bfloat16 parts, to float32 accuracy; there an infinity
- * may make NaN of the outputs and states that it enters, and what lies below
- * 1e-38 in a value is lost. The result equals the recurrence up to rounding, is
- * bitwise reproducible and does not depend on which outputs are wanted. A
- * token's output depends only on the tokens of its own document up to it: where
- * others hold infinities or NaN it has the bits that it has without them, and so
- * have the gradients.
+ * each operand is three bfloat16 parts, to float32 accuracy; what lies below
+ * 1e-38 in a value is lost there. The result equals the recurrence up to
+ * rounding, is bitwise reproducible and does not depend on which outputs are
+ * wanted. An infinity may come out as NaN in the outputs and states that it
+ * enters (a part of what it meets may be 0); of bfloat16 values and of states
+ * it stays one. A token's output depends only on the tokens of its own document
+ * up to it: where others hold infinities or NaN it has the bits that it has
+ * without them, and so have the gradients.
  *
  * Layouts and limits of all calls:
  *   q, k         [batch][seqlen][ngroups][d_k] io, 16-byte aligned

@@ -498,7 +498,8 @@ struct State {
   // 12 heads of 128).
   template <int IO, bool SEQ, typename TileK>
   __device__ __forceinline__ void add(const char* Ks, uint32_t at_col, const Op<IO> (&vf)[2], const float* w_in,
-                                      float keep, uint64_t begins, int g, bool three) {
+                                      float keep, uint64_t begins, int g, int kd, bool three) {
+    bool odd = false;  // a value is not finite
     const int last = SEQ ? last_of(begins) : 0;
 #pragma unroll
     for (int i = 0; i < kTiles; ++i)
@@ -518,6 +519,7 @@ struct State {
       rest(x, first);
       if (IO == 1 && __any(unfit(first, 0.0f) != 0.0f)) {  // an infinity or NaN is whole in its first part: its rest is NaN
         asm volatile("");                                  // a branch, not selects
+        odd = true;
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = x[j] == x[j] ? x[j] : 0.0f;
       }
@@ -544,6 +546,11 @@ struct State {
       } else {
         products(Parts<2>{{p0, p1}});
       }
+    }
+    if (IO == 1 && odd) {  // 0 again beyond kd, where the keys are 0
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+        if (spread(i, 4 * g) >= kd) t[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
     }
   }
 };
@@ -695,7 +702,7 @@ __global__ __launch_bounds__(2 * kThreads) __attribute__((amdgpu_waves_per_eu(IO
         for (int kb = 0; kb < 2; ++kb) vf[kb] = TileV::col(lds + kBufV + par % kTBuf * TileV::kBytes, at_v, 0, kb);
         const float keep = n == kC ? keep_full : power(g2, n);
         const char* Ks = lds + kBufK + par % kTBuf * TileK::kBytes;
-        S.template add<IO, SEQ, TileK>(Ks, at_col, vf, w_in[n < kC], keep, begins, gg, three);
+        S.template add<IO, SEQ, TileK>(Ks, at_col, vf, w_in[n < kC], keep, begins, gg, kd, three);
       }
       if (kSBuf == 1) __syncthreads();  // the chunk's starting state has been read
       put_state(lds + kBufS + (kSBuf == 2 ? par ^ 1 : 0) * TileS::kBytes);
@@ -975,7 +982,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(IO == 
     Op<IO> vf[2];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) vf[kb] = TileV::col(lds + kBufV, at_v, 0, kb);
-    S.template add<IO, SEQ, TileK>(lds, at_col, vf, w_in, keep, begins, g, three);
+    S.template add<IO, SEQ, TileK>(lds, at_col, vf, w_in, keep, begins, g, kd, three);
     __syncthreads();
     kt.store(lds, tid);
     vt.store(lds + kBufV, tid);
