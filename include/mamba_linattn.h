@@ -28,8 +28,8 @@
  * 1e-38 in a value is lost there. The result equals the recurrence up to
  * rounding, is bitwise reproducible and does not depend on which outputs are
  * wanted. An infinity may come out as NaN in the outputs and states that it
- * enters (a part of what it meets may be 0); of bfloat16 values and of states
- * it stays one. A token's output depends only on the tokens of its own document
+ * enters (a part of what it meets may be 0); with bfloat16 io one in v or in a
+ * state stays one. A token's output depends only on the tokens of its own document
  * up to it: where others hold infinities or NaN it has the bits that it has
  * without them, and so have the gradients.
  *
