@@ -1,0 +1,477 @@
+// The short causal convolution in front of a scan, depthwise over time, its
+// gradients and its one-token form.
+//
+// Per batch row and channel, with k taps and x before the first token from the
+// state:
+//   u_t = b + sum_{j<k} w_j x_{t-k+1+j},   y_t = act(u_t).
+// Gradients, with du_t = dy_t act'(u_t):
+//   dx_s = sum_{d<k} w_{k-1-d} du_{s+d},  dw_j = sum_t du_t x_{t-k+1+j},  db = sum_t du_t.
+//
+// Every tensor is read and written once, so all of it is bound by memory
+// traffic. A lane holds 16 bytes' worth of neighbouring channels and walks a run
+// of tokens with the last k - 1 inputs in registers; 32 lanes side by side read
+// 512 bytes of a token, and a workgroup's eight such groups walk runs that
+// follow one another. What two runs both read (k - 1 tokens) comes from the caches.
+// The backward walks the same way, k - 1 tokens further: a token's dx is
+// complete, and leaves, k - 1 tokens after it. u is computed again rather than
+// kept. Sums over tokens stay in registers and leave as one partial sum per
+// workgroup, which a second kernel adds in a fixed order.
+#include <algorithm>
+
+#include "conv_internal.h"
+#include "row_device.h"
+
+namespace mscan {
+
+namespace {
+
+constexpr int kThreads = 256;
+// Lanes side by side along a token, and runs of a workgroup.
+template <int V>
+struct Shape {
+  static constexpr int kLn = V > 1 ? 32 : 64, kSub = kThreads / kLn;
+};
+
+struct ConvArgs {
+  int32_t batch, seqlen, channels, activation, cols, nblk, run, nruns;  // nruns: of one batch row
+  int64_t runs, x_row;
+  const void* x;
+  const int32_t* seq_idx;
+  const float *weight, *bias, *state_in, *dstate_out;
+  int32_t first[kConvMaxParts];  // each part's first channel (channels behind the last part)
+  void* part[kConvMaxParts];
+  int64_t part_row[kConvMaxParts];
+  float *state_out, *dstate_in;
+  void* dx;
+  float *pw, *pb;
+};
+
+// A lane's place in a part: the address of its channels in the row of token 0.
+template <typename T>
+struct PartAt {
+  T* p;
+  int64_t row;
+  __device__ __forceinline__ PartAt(const ConvArgs& a, int c) {
+    int i = 0;
+#pragma unroll
+    for (int j = 1; j < kConvMaxParts; ++j) i = c >= a.first[j] ? j : i;
+    p = static_cast<T*>(a.part[i]) + (c - a.first[i]);
+    row = a.part_row[i];
+  }
+};
+
+template <int IO, int V>
+__device__ __forceinline__ Vec<IO, V> read(const typename Io<IO>::T* p) {
+  return *reinterpret_cast<const Vec<IO, V>*>(p);
+}
+template <int IO, int V>
+__device__ __forceinline__ void write(typename Io<IO>::T* p, const float (&o)[V]) {
+  if constexpr (V == 1) {
+    Io<IO>::store(p, o[0]);
+  } else if constexpr (IO == 1) {
+    *reinterpret_cast<u4*>(p) = __builtin_bit_cast(u4, frag_regs<1>(f4{o[0], o[1], o[2], o[3]}, f4{o[4], o[5], o[6], o[7]}).v);
+  } else {
+    *reinterpret_cast<f4*>(p) = f4{o[0], o[1], o[2], o[3]};
+  }
+}
+
+template <int V, int K>
+struct Params {
+  float w[K][V], b[V];
+  __device__ __forceinline__ Params(const ConvArgs& a, int c) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+      for (int j = 0; j < K; ++j) w[j][i] = a.weight[static_cast<int64_t>(c + i) * K + j];
+      b[i] = a.bias ? a.bias[c + i] : 0.0f;
+    }
+  }
+  // u of a token whose input is x, with the K - 1 inputs before it in `past`
+  __device__ __forceinline__ void sum(const float (&past)[K - 1][V], const float (&x)[V], float (&u)[V]) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      u[i] = b[i];
+#pragma unroll
+      for (int j = 0; j < K - 1; ++j) u[i] = fmaf(w[j][i], past[j][i], u[i]);
+      u[i] = fmaf(w[K - 1][i], x[i], u[i]);
+    }
+  }
+};
+
+// The inputs before a run's first token, oldest first, and how many of them are
+// of that token's document (K - 1 where the document began earlier).
+template <int IO, int V, int K, bool SEQ>
+struct Past {
+  float x[K - 1][V];
+  int age;
+  __device__ __forceinline__ Past(const ConvArgs& a, const typename Io<IO>::T* row0, int b, int t0, int c) {
+    age = K - 1;
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) {
+      const int t = t0 - (K - 1) + j;
+      if (t >= 0) {
+        unpack<IO, V>(read<IO, V>(row0 + t * a.x_row), x[j]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          x[j][i] = a.state_in ? a.state_in[(static_cast<int64_t>(b) * a.channels + c + i) * (K - 1) + t + K - 1] : 0.0f;
+      }
+      if (SEQ) meet(t > 0 && differs(a, b, t));
+      if (SEQ && age == 0)
+#pragma unroll
+        for (int q = 0; q < j; ++q) clear(q);
+    }
+  }
+  static __device__ __forceinline__ bool differs(const ConvArgs& a, int b, int t) {
+    const int32_t* id = a.seq_idx + static_cast<int64_t>(b) * a.seqlen + t;
+    return id[0] != id[-1];
+  }
+  __device__ __forceinline__ void clear(int q) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[q][i] = 0.0f;
+  }
+  // A token comes, at which a document begins or does not.
+  __device__ __forceinline__ void meet(bool begins) { age = begins ? 0 : age < K - 1 ? age + 1 : age; }
+  __device__ __forceinline__ void begin(bool begins) {
+    meet(begins);
+#pragma unroll
+    for (int q = 0; q < K - 1; ++q)
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[q][i] = begins ? 0.0f : x[q][i];  // chosen: whatever it was
+  }
+  __device__ __forceinline__ void push(const float (&v)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+      for (int q = 0; q < K - 2; ++q) x[q][i] = x[q + 1][i];
+      x[K - 2][i] = v[i];
+    }
+  }
+};
+
+// The activation's derivative: of silu, s + u s (1 - s), also at +inf, where it
+// is 1 (and not as infinity times 0).
+__device__ __forceinline__ float slope(int kind, float u) {
+  const Sig g = sigmoid(u);
+  return kind == kActNone ? 1.0f : fmaf(fminf(silu_of(u, g.s), 0x1.fffffep127f), g.c, g.s);
+}
+
+constexpr int kU = 4;  // tokens in flight
+
+template <int IO, int V, int K, bool SEQ>
+__global__ __launch_bounds__(kThreads) void conv_fwd_kernel(const ConvArgs a) {
+  using T = typename Io<IO>::T;
+  using S = Shape<V>;
+  const int sub = threadIdx.x / S::kLn;
+  const int col = blockIdx.x % a.cols, blk = blockIdx.x / a.cols;
+  const int c = (col * S::kLn + static_cast<int>(threadIdx.x % S::kLn)) * V;
+  if (c >= a.channels) return;
+  const Params<V, K> par(a, c);
+  const PartAt<T> part(a, c);
+  for (int64_t r = static_cast<int64_t>(blk) * S::kSub + sub; r < a.runs; r += static_cast<int64_t>(a.nblk) * S::kSub) {
+    const int b = static_cast<int>(r / a.nruns), t0 = static_cast<int>(r - static_cast<int64_t>(b) * a.nruns) * a.run;
+    const int t1 = min(t0 + a.run, a.seqlen);
+    const int64_t first = static_cast<int64_t>(b) * a.seqlen;
+    const T* row0 = static_cast<const T*>(a.x) + first * a.x_row + c;
+    Vec<IO, V> now[kU], next[kU];
+    auto fetch = [&](int t, Vec<IO, V>(&v)[kU]) {
+#pragma unroll
+      for (int i = 0; i < kU; ++i) v[i] = read<IO, V>(row0 + min(t + i, t1 - 1) * a.x_row);
+    };
+    fetch(t0, now);
+    Past<IO, V, K, SEQ> past(a, row0, b, t0, c);
+    T* out = part.p + (first + t0) * part.row;
+    for (int t = t0; t < t1; t += kU) {
+      fetch(min(t + kU, t1 - 1), next);
+#pragma unroll
+      for (int i = 0; i < kU; ++i) {
+        if (t + i >= t1) break;
+        float x[V], u[V];
+        unpack<IO, V>(now[i], x);
+        if (SEQ) past.begin(t + i > 0 && past.differs(a, b, t + i));
+        par.sum(past.x, x, u);
+        past.push(x);
+#pragma unroll
+        for (int e = 0; e < V; ++e) u[e] = act(a.activation, u[e]);
+        write<IO, V>(out, u);
+        out += part.row;
+      }
+#pragma unroll
+      for (int i = 0; i < kU; ++i) now[i] = next[i];
+    }
+    if (a.state_out && t1 == a.seqlen)
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j)
+          a.state_out[(static_cast<int64_t>(b) * a.channels + c + i) * (K - 1) + j] = past.x[j][i];
+  }
+}
+
+template <int IO, int V, int K, bool SEQ>
+__global__ __launch_bounds__(kThreads) void conv_bwd_kernel(const ConvArgs a) {
+  using T = typename Io<IO>::T;
+  using S = Shape<V>;
+  __shared__ float join[S::kSub][S::kLn * V];
+  const int sub = threadIdx.x / S::kLn, lane = threadIdx.x % S::kLn;
+  const int col = blockIdx.x % a.cols, blk = blockIdx.x / a.cols;
+  const int c = (col * S::kLn + lane) * V;
+  float dw[K][V], db[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    db[i] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < K; ++j) dw[j][i] = 0.0f;
+  }
+  if (c < a.channels) {
+    const Params<V, K> par(a, c);
+    const PartAt<const T> part(a, c);
+    for (int64_t r = static_cast<int64_t>(blk) * S::kSub + sub; r < a.runs; r += static_cast<int64_t>(a.nblk) * S::kSub) {
+      const int b = static_cast<int>(r / a.nruns), t0 = static_cast<int>(r - static_cast<int64_t>(b) * a.nruns) * a.run;
+      const int t1 = min(t0 + a.run, a.seqlen);  // the run's own tokens
+      const int64_t first = static_cast<int64_t>(b) * a.seqlen, state0 = (static_cast<int64_t>(b) * a.channels + c) * (K - 1);
+      const T* row0 = static_cast<const T*>(a.x) + first * a.x_row + c;
+      const T* dy0 = part.p + first * part.row;
+      T* out = static_cast<T*>(a.dx) + (first + t0) * a.channels + c;
+      const int last = a.seqlen - 1;
+      Vec<IO, V> now[kU], next[kU], dnow[kU], dnext[kU];
+      auto fetch = [&](int t, Vec<IO, V>(&v)[kU], Vec<IO, V>(&d)[kU]) {
+#pragma unroll
+        for (int i = 0; i < kU; ++i) {
+          v[i] = read<IO, V>(row0 + min(t + i, last) * a.x_row);
+          d[i] = read<IO, V>(dy0 + min(t + i, last) * part.row);
+        }
+      };
+      fetch(t0, now, dnow);
+      Past<IO, V, K, SEQ> past(a, row0, b, t0, c);
+      float acc[K][V];  // dx of the K latest tokens, oldest first
+#pragma unroll
+      for (int d = 0; d < K; ++d)
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[d][i] = 0.0f;
+      const int stop = t1 + K - 1;
+      for (int t = t0; t < stop; t += kU) {
+        fetch(t + kU, next, dnext);
+#pragma unroll
+        for (int i = 0; i < kU; ++i) {
+          const int at = t + i;
+          if (at >= stop) break;
+          if (at <= last) {
+            float x[V], du[V], u[V];
+            unpack<IO, V>(now[i], x);
+            unpack<IO, V>(dnow[i], du);
+            if (SEQ) past.begin(at > 0 && past.differs(a, b, at));
+            par.sum(past.x, x, u);
+            const bool own = at < t1;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+              du[e] *= slope(a.activation, u[e]);
+              const float d = own ? du[e] : 0.0f;
+              db[e] += d;
+#pragma unroll
+              for (int j = 0; j < K - 1; ++j) dw[j][e] = own ? fmaf(d, past.x[j][e], dw[j][e]) : dw[j][e];
+              dw[K - 1][e] = own ? fmaf(d, x[e], dw[K - 1][e]) : dw[K - 1][e];
+#pragma unroll
+              for (int d = 0; d < K; ++d) {  // the token d before this one: tap K - 1 - d met it
+                const float to = acc[K - 1 - d][e];
+                acc[K - 1 - d][e] = !SEQ || d <= past.age ? fmaf(par.w[K - 1 - d][e], du[e], to) : to;
+              }
+            }
+            past.push(x);
+          }
+          const int s = at - (K - 1);  // complete; before t0 it is another run's, or the state's
+          const int in_state = s - (a.seqlen - (K - 1));
+          if (a.dstate_out && in_state >= 0 && (!SEQ || last - s <= past.age))
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[0][e] += a.dstate_out[state0 + e * (K - 1) + in_state];
+          if (s >= t0) {
+            write<IO, V>(out, acc[0]);
+            out += a.channels;
+          } else if (t0 == 0 && a.dstate_in) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) a.dstate_in[state0 + e * (K - 1) + at] = acc[0][e];
+          }
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+#pragma unroll
+            for (int d = 0; d < K - 1; ++d) acc[d][e] = acc[d + 1][e];
+            acc[K - 1][e] = 0.0f;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kU; ++i) {
+          now[i] = next[i];
+          dnow[i] = dnext[i];
+        }
+      }
+    }
+  }
+  // the workgroup's runs, one after the other
+#pragma unroll
+  for (int j = 0; j <= K; ++j) {
+    if (j == K && !a.pb) break;
+#pragma unroll
+    for (int i = 0; i < V; ++i) join[sub][lane * V + i] = j < K ? dw[j < K ? j : 0][i] : db[i];
+    __syncthreads();
+    const int e = threadIdx.x, ch = col * S::kLn * V + e;
+    if (e < S::kLn * V && ch < a.channels) {
+      float s = join[0][e];
+#pragma unroll
+      for (int q = 1; q < S::kSub; ++q) s += join[q][e];
+      const int64_t to = static_cast<int64_t>(blk) * a.channels + ch;
+      (j < K ? a.pw[to * K + j] : a.pb[to]) = s;
+    }
+    __syncthreads();
+  }
+}
+
+// One token: a lane a channel.
+template <int IO, int K>
+__global__ __launch_bounds__(kThreads) void conv_step_kernel(const ConvArgs a) {
+  using T = typename Io<IO>::T;
+  const int64_t n = static_cast<int64_t>(a.batch) * a.channels;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n;
+       i += static_cast<int64_t>(gridDim.x) * kThreads) {
+    const int b = static_cast<int>(i / a.channels), c = static_cast<int>(i - static_cast<int64_t>(b) * a.channels);
+    const Params<1, K> par(a, c);
+    const PartAt<T> part(a, c);
+    float past[K - 1][1], x[1], u[1];
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) past[j][0] = a.state_in[i * (K - 1) + j];
+    x[0] = Io<IO>::load(static_cast<const T*>(a.x) + b * a.x_row + c);
+    par.sum(past, x, u);
+    Io<IO>::store(part.p + b * part.row, act(a.activation, u[0]));
+#pragma unroll
+    for (int j = 0; j < K - 2; ++j) a.state_out[i * (K - 1) + j] = past[j + 1][0];
+    a.state_out[i * (K - 1) + K - 2] = x[0];
+  }
+}
+
+// Tokens of a run, runs of a batch row and workgroups that share the runs of
+// `cols` column groups.
+struct Split {
+  int32_t run, nruns, cols, nblk;
+  int64_t runs;
+};
+Split split(int32_t batch, int32_t seqlen, int32_t channels, int vec, bool bwd) {
+  Split s{};
+  const int ln = vec > 1 ? 32 : 64, sub = kThreads / ln;
+  s.cols = (channels + ln * vec - 1) / (ln * vec);
+  s.run = bwd ? 32 : 16;
+  auto units = [&]() {
+    s.nruns = (seqlen + s.run - 1) / s.run;
+    s.runs = static_cast<int64_t>(batch) * s.nruns;
+    return (s.runs + sub - 1) / sub;
+  };
+  // short runs where there are few tokens
+  while (s.run > 4 && units() * s.cols < 512) s.run /= 2;
+  const int64_t all = units(), slots = bwd ? 1024 : int64_t{1} << 22, most = std::max<int64_t>(1, slots / s.cols);
+  const int64_t turns = (all + most - 1) / most;
+  s.nblk = static_cast<int32_t>((all + turns - 1) / turns);
+  return s;
+}
+
+int full(int32_t io_dtype) { return io_dtype == 0 ? 4 : 8; }
+
+ConvArgs args(const ConvCall& c) {
+  ConvArgs a{};
+  a.batch = c.batch;
+  a.seqlen = c.seqlen;
+  a.channels = c.channels;
+  a.activation = c.activation;
+  a.x_row = c.x_row;
+  a.x = c.x;
+  a.seq_idx = c.seq_idx;
+  a.weight = c.weight;
+  a.bias = c.bias;
+  a.state_in = c.state_in;
+  a.dstate_out = c.dstate_out;
+  a.state_out = c.state_out;
+  a.dstate_in = c.dstate_in;
+  a.dx = c.dx;
+  int32_t first = 0;
+  for (int i = 0; i < kConvMaxParts; ++i) {
+    a.first[i] = i < c.parts ? first : c.channels;
+    if (i >= c.parts) continue;
+    a.part[i] = c.part[i];
+    a.part_row[i] = c.part_row[i];
+    first += c.part_channels[i];
+  }
+  return a;
+}
+
+bool can_vec(const ConvCall& c) {
+  const int v = full(c.io_dtype);
+  auto fits = [&](const void* p, int64_t row) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && row % v == 0; };
+  bool ok = fits(c.x, c.x_row) && c.channels % v == 0 && (!c.dx || fits(c.dx, c.channels));
+  for (int i = 0; i < c.parts; ++i) ok = ok && fits(c.part[i], c.part_row[i]) && c.part_channels[i] % v == 0;
+  return ok;
+}
+
+template <int IO, int V, int K>
+hipError_t launch_taps(const ConvCall& c, ConvArgs a) {
+  const Split s = split(c.batch, c.seqlen, c.channels, V, c.dx != nullptr);
+  a.cols = s.cols;
+  a.nblk = s.nblk;
+  a.run = s.run;
+  a.nruns = s.nruns;
+  a.runs = s.runs;
+  const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(s.cols) * s.nblk)), block(kThreads);
+  if (!c.dx) {
+    if (c.seq_idx)
+      hipLaunchKernelGGL((conv_fwd_kernel<IO, V, K, true>), grid, block, 0, c.stream, a);
+    else
+      hipLaunchKernelGGL((conv_fwd_kernel<IO, V, K, false>), grid, block, 0, c.stream, a);
+    return hipGetLastError();
+  }
+  a.pw = c.sums;
+  a.pb = c.dbias ? c.sums + static_cast<size_t>(s.nblk) * c.channels * K : nullptr;
+  if (c.seq_idx)
+    hipLaunchKernelGGL((conv_bwd_kernel<IO, V, K, true>), grid, block, 0, c.stream, a);
+  else
+    hipLaunchKernelGGL((conv_bwd_kernel<IO, V, K, false>), grid, block, 0, c.stream, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return launch_part_sums(s.nblk, c.channels * K, a.pw, c.dweight, c.channels, a.pb, c.dbias, c.stream);
+}
+
+template <int IO, int V>
+hipError_t launch_vec(const ConvCall& c, const ConvArgs& a) {
+  return c.taps == 2 ? launch_taps<IO, V, 2>(c, a) : c.taps == 3 ? launch_taps<IO, V, 3>(c, a) : launch_taps<IO, V, 4>(c, a);
+}
+
+template <int IO>
+hipError_t launch_step_io(const ConvCall& c, const ConvArgs& a) {
+  const int64_t blocks = (static_cast<int64_t>(c.batch) * c.channels + kThreads - 1) / kThreads;
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(blocks, 1 << 20))), block(kThreads);
+  if (c.taps == 2)
+    hipLaunchKernelGGL((conv_step_kernel<IO, 2>), grid, block, 0, c.stream, a);
+  else if (c.taps == 3)
+    hipLaunchKernelGGL((conv_step_kernel<IO, 3>), grid, block, 0, c.stream, a);
+  else
+    hipLaunchKernelGGL((conv_step_kernel<IO, 4>), grid, block, 0, c.stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t conv_part_floats(int32_t batch, int32_t seqlen, int32_t channels, int32_t taps, int32_t io_dtype) {
+  // the call may take either form, by the alignment of its tensors
+  const size_t v = split(batch, seqlen, channels, full(io_dtype), true).nblk;
+  const size_t s = split(batch, seqlen, channels, 1, true).nblk;
+  return (v > s ? v : s) * static_cast<size_t>(channels) * (taps + 1);
+}
+
+hipError_t launch_conv(const ConvCall& c) {
+  const ConvArgs a = args(c);
+  const bool vec = can_vec(c);
+  if (c.io_dtype == 0) return vec ? launch_vec<0, 4>(c, a) : launch_vec<0, 1>(c, a);
+  return vec ? launch_vec<1, 8>(c, a) : launch_vec<1, 1>(c, a);
+}
+
+hipError_t launch_conv_step(const ConvCall& c) {
+  const ConvArgs a = args(c);
+  return c.io_dtype == 0 ? launch_step_io<0>(c, a) : launch_step_io<1>(c, a);
+}
+
+}  // namespace mscan
