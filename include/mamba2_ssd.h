@@ -90,6 +90,40 @@ int mamba2_ssd_step(int32_t batch, int32_t nheads, int32_t headdim, int32_t d_st
                     const float* dt_bias, const float* A, const float* D, const float* state_in, void* y,
                     float* state_out, void* stream);
 
+/* Bytes of device workspace mamba2_ssd_bwd needs (0 for shapes it rejects): a
+   float32 state and its gradient per (batch row, chunk of 256 steps, head), and
+   some 12 KB more; dB and dC in float32, several times where a group's heads are
+   split over workgroups. */
+size_t mamba2_ssd_bwd_workspace_bytes(int32_t batch, int32_t seqlen, int32_t nheads, int32_t headdim, int32_t d_state,
+                                      int32_t ngroups, int32_t io_dtype);
+
+/*
+ * Gradients of mamba2_ssd_fwd (seq_idx NULL) or mamba2_ssd_fwd_seq with the same
+ * inputs; nothing of the forward call is kept.
+ *   x, B, C, dy      as in the forward (dy like y), rows (batch, step) *_stride
+ *                    elements apart, so that they can be columns of a wider tensor
+ *                    (at least a row, at most 2^24); pointers and rows 16-byte
+ *                    aligned
+ *   dt               likewise, element aligned
+ *   dt_bias, A, D    [nheads] float32; A at most 0
+ *   state_in         the forward's, or NULL (zeros)
+ *   dstate_out       gradient of the forward's state_out, like state_in, or NULL (zeros)
+ *   dx, ddt, dB, dC  gradients, io, contiguous, 16-byte aligned (ddt: element
+ *                    aligned); dB and dC are summed over the heads of a group
+ *   ddt_bias, dA, dD [nheads] float32
+ *   dstate_in        gradient of state_in, or NULL (not written)
+ *   workspace        >= mamba2_ssd_bwd_workspace_bytes(...) bytes, 256-byte aligned
+ * Same shape limits as mamba2_ssd_fwd. Sums over steps of delta A are float64;
+ * float32 values that meet the matrix cores keep 16 bits at least. Outputs
+ * overlap nothing. Results are bitwise reproducible run to run.
+ */
+int mamba2_ssd_bwd(int32_t batch, int32_t seqlen, int32_t nheads, int32_t headdim, int32_t d_state, int32_t ngroups,
+                   int32_t io_dtype, const void* x, int64_t x_stride, const void* dt, int64_t dt_stride, const void* B,
+                   int64_t B_stride, const void* C, int64_t C_stride, const int32_t* seq_idx, const float* dt_bias,
+                   const float* A, const float* D, const float* state_in, const void* dy, int64_t dy_stride,
+                   const float* dstate_out, void* dx, void* ddt, void* dB, void* dC, float* ddt_bias, float* dA,
+                   float* dD, float* dstate_in, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -19,7 +19,7 @@ EXPORTS = ("mamba_scan_abi_version", "mamba_scan_status_str", "mamba_scan_last_e
            "mamba_scan_call_count", "mamba_scan_fwd_workspace_bytes", "mamba_scan_fwd", "mamba_scan_fwd_seq",
            "mamba_scan_ckpt_bytes", "mamba_scan_fwd_ckpt", "mamba_scan_bwd_workspace_bytes", "mamba_scan_bwd",
            "mamba_scan_bwd_ckpt_workspace_bytes", "mamba_scan_bwd_ckpt", "mamba_scan_step", "mamba2_ssd_fwd_workspace_bytes",
-           "mamba2_ssd_fwd", "mamba2_ssd_fwd_seq", "mamba2_ssd_step", "mamba_scan_fwd_noalloc", "mamba_scan_fwd_xc",
+           "mamba2_ssd_fwd", "mamba2_ssd_fwd_seq", "mamba2_ssd_bwd_workspace_bytes", "mamba2_ssd_bwd", "mamba2_ssd_step", "mamba_scan_fwd_noalloc", "mamba_scan_fwd_xc",
            "mamba_scan_step_xc", "mamba_scan_step_xc_dtproj", "mamba_scan_fwd_xc_dtproj")
 NOALLOC_SCRATCH_BYTES = 8 << 20  # MAMBA_SCAN_NOALLOC_SCRATCH_BYTES
 # Every symbol include/mamba_scan_testing.h declares (test suites only).
@@ -82,6 +82,11 @@ def load():
     lib.mamba2_ssd_fwd.argtypes = [i32] * 7 + [vp] * 10 + [vp, sz, vp]
     lib.mamba2_ssd_fwd_seq.restype = ctypes.c_int
     lib.mamba2_ssd_fwd_seq.argtypes = [i32] * 7 + [vp] * 11 + [vp, sz, vp]
+    i64 = ctypes.c_int64
+    lib.mamba2_ssd_bwd_workspace_bytes.restype = sz
+    lib.mamba2_ssd_bwd_workspace_bytes.argtypes = [i32] * 7
+    lib.mamba2_ssd_bwd.restype = ctypes.c_int
+    lib.mamba2_ssd_bwd.argtypes = [i32] * 7 + [vp, i64] * 4 + [vp] * 5 + [vp, i64] + [vp] * 10 + [sz, vp]
     lib.mamba2_ssd_step.restype = ctypes.c_int
     lib.mamba2_ssd_step.argtypes = [i32] * 6 + [vp] * 10 + [vp]
     lib.mamba_scan_step.restype = ctypes.c_int
@@ -234,6 +239,19 @@ def mamba2_ssd_fwd_seq(batch, seqlen, nheads, headdim, d_state, ngroups, io_dtyp
                                 dt_bias, A, D, state_in, y, state_out, workspace, workspace_bytes, stream)
     if check:
         _check(lib, st, "mamba2_ssd_fwd_seq")
+    return st
+
+
+def mamba2_ssd_bwd_workspace_bytes(batch, seqlen, nheads, headdim, d_state, ngroups, io_dtype):
+    return int(load().mamba2_ssd_bwd_workspace_bytes(batch, seqlen, nheads, headdim, d_state, ngroups, io_dtype))
+
+
+def mamba2_ssd_bwd(*args, check=True):
+    """Raw call with integer device addresses (0 for NULL), in the order of include/mamba2_ssd.h."""
+    lib = load()
+    st = lib.mamba2_ssd_bwd(*args)
+    if check:
+        _check(lib, st, "mamba2_ssd_bwd")
     return st
 
 

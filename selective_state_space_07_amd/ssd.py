@@ -1,5 +1,5 @@
 """torch-tensor front end of the Mamba-2 SSD scan in libmamba_scan (`ssd_fwd`,
-and `ssd_step` for one token).
+its gradients `ssd_bwd`, and `ssd_step` for one token).
 
 Marshalling only: checks devices, dtypes and shapes, makes tensors contiguous,
 allocates outputs and the workspace, and passes raw device addresses plus
@@ -10,6 +10,7 @@ import torch
 
 from . import _binding as _b
 from .api import _IO, _addr, _dev, _io, check_out, check_workspace
+from .linattn import _f32, _ids, _io_of, _rows, launch, scratch
 
 
 def ssd_workspace_bytes(batch, seqlen, nheads, headdim, d_state, ngroups, dtype):
@@ -67,6 +68,54 @@ def ssd_fwd(x, dt, B, C, dt_bias, A, D, state=None, *, out=None, state_out=None,
                               _addr(C), _addr(seq_idx), _addr(dt_bias), _addr(A), _addr(D), _addr(state), _addr(y),
                               _addr(state_out), _addr(workspace), ws_bytes, stream)
     return y, state_out
+
+
+def ssd_bwd_workspace_bytes(batch, seqlen, nheads, headdim, d_state, ngroups, dtype):
+    return _b.mamba2_ssd_bwd_workspace_bytes(batch, seqlen, nheads, headdim, d_state, ngroups, _IO[dtype])
+
+
+def ssd_bwd(x, dt, B, C, dt_bias, A, D, dy, state=None, dstate=None, *, seq_idx=None, workspace=None):
+    """Gradients of `ssd_fwd` given dy = dL/dy (like x) and dstate = dL/d(final state) ([batch, nheads, headdim, d_state]
+    float32, or None for zeros); the other arguments are the forward's, with A at most 0. x, dt, B, C and dy may be
+    columns of wider tensors; they are read in place.
+
+    Returns a dict: dx, ddt, dB, dC (dtype and shape of x, dt, B, C; dB and dC are summed over the heads of a group),
+    ddt_bias, dA, dD ([nheads] float32) and, where a state is given, dstate (float32, its gradient)."""
+    lib = _b.load()
+    io, dtype, dev = _io_of(x, "x")
+    x, xp, xs = _rows(x, "x", dtype, dev, 2, 16)
+    dt, dtp, dts = _rows(dt, "dt", dtype, dev, 2, x.element_size())
+    B, Bp, Bs = _rows(B, "B", dtype, dev, 2, 16)
+    C, Cp, Cs = _rows(C, "C", dtype, dev, 2, 16)
+    dy, dyp, dys = _rows(dy, "dy", dtype, dev, 2, 16)
+    if x.dim() != 4 or B.dim() != 4:
+        raise _b.MambaScanError(2, "x must be [batch, seqlen, nheads, headdim] and B [batch, seqlen, ngroups, d_state]")
+    batch, seqlen, nheads, headdim = x.shape
+    ngroups, d_state = B.shape[2:]
+    if dt.shape != (batch, seqlen, nheads) or C.shape != B.shape or B.shape[:2] != (batch, seqlen) or dy.shape != x.shape:
+        raise _b.MambaScanError(2, "shape mismatch between x %s, dy %s, dt %s, B %s and C %s" %
+                                tuple(tuple(t.shape) for t in (x, dy, dt, B, C)))
+    state_shape = (batch, nheads, headdim, d_state)
+    dt_bias, dbp = _f32(dt_bias, "dt_bias", dev, (nheads,))
+    A, Ap = _f32(A, "A", dev, (nheads,))
+    D, Dp = _f32(D, "D", dev, (nheads,))
+    state, sp = _f32(state, "state", dev, state_shape)
+    dstate, dsp = _f32(dstate, "dstate", dev, state_shape)
+    seq_idx, ip = _ids(seq_idx, dev, batch, seqlen)
+    grads = {"dx": x.new_empty(x.shape), "ddt": x.new_empty(dt.shape), "dB": x.new_empty(B.shape),
+             "dC": x.new_empty(B.shape)}
+    for n in ("ddt_bias", "dA", "dD"):
+        grads[n] = x.new_empty(nheads, dtype=torch.float32)
+    dsi = 0
+    if state is not None:
+        grads["dstate"] = x.new_empty(state_shape, dtype=torch.float32)
+        dsi = grads["dstate"].data_ptr()
+    sizes = (batch, seqlen, nheads, headdim, d_state, ngroups, io)
+    ws, ws_bytes, keep = scratch(workspace, lib.mamba2_ssd_bwd_workspace_bytes(*sizes), x)
+    launch(dev, "mamba2_ssd_bwd", lib, lib.mamba2_ssd_bwd, *sizes, xp, xs, dtp, dts, Bp, Bs, Cp, Cs, ip, dbp, Ap, Dp, sp,
+           dyp, dys, dsp, *(grads[n].data_ptr() for n in ("dx", "ddt", "dB", "dC", "ddt_bias", "dA", "dD")), dsi, ws,
+           ws_bytes)
+    return grads
 
 
 def ssd_step(x, dt, B, C, dt_bias, A, D, state, *, inplace=False, out=None):
