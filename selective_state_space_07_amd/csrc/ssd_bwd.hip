@@ -242,6 +242,24 @@ struct StateWay {
       }
     }
   }
+  // what store<NP> put there of v[q]
+  template <int NP>
+  static __device__ __forceinline__ f4 back(const char* lds, int q, int tid) {
+    using L = Lds<IO, N>;
+    const uint32_t i = tid + q * NT;
+    const char* from = lds + L::at(i / (N / 4), i % (N / 4) * 4 * L::kB);
+    f4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (IO == 1) {
+#pragma unroll
+      for (int p = NP - 1; p >= 0; --p) {
+        const u2 w = *reinterpret_cast<const u2*>(from + p * L::kBytes);
+        o += f4{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u)};
+      }
+    } else {
+      o = *reinterpret_cast<const f4*>(from);
+    }
+    return o;
+  }
 };
 
 struct SbArgs {
@@ -259,7 +277,7 @@ struct SbArgs {
   double* cs;          // [bch][256]
   float* delta;        // [bch][256]
   int32_t *begin, *next;  // [batch][chunk][256]: the latest document begin up to a token (-1: none), the first behind it (256)
-  float* dot;          // [bch][8]: shares of <R, S>
+  float* dot;          // [bch][16]: shares of <R, S>
   float* tok;          // [kTokSums][bch][256]
   int64_t tok_step;
   float *dBp, *dCp;    // [hsplit][batch][seqlen][ngroups][N], where hsplit > 1
@@ -448,7 +466,7 @@ template <int IO, int N>
 struct CarryLds {
   static constexpr int kTok = IO == 1 ? 2 : 1;                     // tokens of a lane
   static constexpr int kRows = 128 * kTok;                         // of a workgroup
-  static constexpr int kPad = 8;                                   // bytes behind a row of C (B)
+  static constexpr int kPad = 16;                                  // bytes behind a row of C (B)
   static constexpr uint32_t kRow = N * sizeof(typename Io<IO>::T) + kPad, kState = LdsState<IO, N, 3>::kBytes;
   static constexpr uint32_t kBytes = kState + kRows * kRow;
 };
@@ -523,28 +541,25 @@ __device__ __forceinline__ void ssdb_carry(const SbArgs& a, int u, char* lds) {
     const int64_t bch = bc * a.nheads + h;
     __syncthreads();  // the last head's state has been read
     way.template store<3>(lds, tid);
-    if (OF_C && from == 0) {  // a thread's share of <R, S>
-      Way r;
-      r.load(a.R + bch * (kP * N), tid);
-      float s = 0.0f;
+    // half of <R, S> is of either state's workgroup; what it takes of the other state comes before the next head's
+    constexpr int kDot = Way::kN / 2;
+    f4 other[kDot];
+    if (from == 0) {
+      const f4* src = reinterpret_cast<const f4*>((OF_C ? a.R : a.S) + bch * (kP * N)) + tid + (OF_C ? 0 : kDot * kMain);
 #pragma unroll
-      for (int q = 0; q < Way::kN; ++q)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s = fmaf(way.v[q][j], r.v[q][j], s);
-      s = lanes_sum(s, 64);
-      if (lane == 0) a.dot[bch * 8 + wave] = s;
+      for (int q = 0; q < kDot; ++q) other[q] = src[q * kMain];
     }
     Frag<IO> now[kTok][2];
-    float e[kTok], d[kTok];
+    float e[kTok], de[kTok];
 #pragma unroll
     for (int k = 0; k < kTok; ++k) {
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) now[k][kb] = open[k] ? f[k][kb] : frag_zero<IO>();
+      for (int kb = 0; kb < 2; ++kb) now[k][kb] = f[k][kb];
       e[k] = decayed(OF_C ? cs[k] : end - cs[k]);
-      d[k] = delta[k];
+      de[k] = OF_C ? e[k] : delta[k] * e[k];
     }
-    fetch(h + 1 < h1 ? h + 1 : h);
     __syncthreads();
+    fetch(h + 1 < h1 ? h + 1 : h);
     float share[kTok] = {};
     int l = l15, gg = g;
 #pragma unroll
@@ -578,19 +593,27 @@ __device__ __forceinline__ void ssdb_carry(const SbArgs& a, int u, char* lds) {
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float t = open[k] ? v[k][j] * e[k] : 0.0f;
-          if (OF_C)
-            sum[k][nt][j] += t;
-          else
-            sum[k][nt][j] = fmaf(t, d[k], sum[k][nt][j]);
-          share[k] = fmaf(t, open[k] ? with[j] : 0.0f, share[k]);
+          sum[k][nt][j] = fmaf(v[k][j], de[k], sum[k][nt][j]);
+          share[k] = fmaf(v[k][j], with[j], share[k]);
         }
       }
     }
+    // a token that the state does not reach has sums of its own too, and none of them counts
 #pragma unroll
     for (int k = 0; k < kTok; ++k) {
-      share[k] = over_g(share[k]);
-      if (g == 0) a.tok[(OF_C ? kOfS : kOfR) * a.tok_step + bch * kQ + at[k]] = share[k];
+      share[k] = over_g(share[k]) * e[k];
+      if (g == 0) a.tok[(OF_C ? kOfS : kOfR) * a.tok_step + bch * kQ + at[k]] = open[k] ? share[k] : 0.0f;
+    }
+    if (from == 0) {
+      float s = 0.0f;
+#pragma unroll
+      for (int q = 0; q < kDot; ++q) {
+        const f4 own = Way::template back<3>(lds, OF_C ? q : kDot + q, tid);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s = fmaf(own[j], other[q][j], s);
+      }
+      s = lanes_sum(s, 64);
+      if (lane == 0) a.dot[bch * 16 + (OF_C ? 0 : 8) + wave] = s;
     }
   }
   float* out = (OF_C ? a.dCc : a.dBc) + hs * (static_cast<int64_t>(a.batch) * a.seqlen * a.ngroups * N);
@@ -599,8 +622,12 @@ __device__ __forceinline__ void ssdb_carry(const SbArgs& a, int u, char* lds) {
     if (at[k] >= valid) continue;
     float* to = out + ((row0 + at[k]) * a.ngroups + grp) * N + 4 * g;
 #pragma unroll
-    for (int nt = 0; nt < kNt; ++nt)
-      *reinterpret_cast<f4*>(to + 16 * nt) = f4{sum[k][nt][0], sum[k][nt][1], sum[k][nt][2], sum[k][nt][3]};
+    for (int nt = 0; nt < kNt; ++nt) {
+      f4 v;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = open[k] ? sum[k][nt][j] : 0.0f;
+      *reinterpret_cast<f4*>(to + 16 * nt) = v;
+    }
   }
 }
 template <int IO, int N, bool SEQ>
@@ -614,8 +641,9 @@ __global__ __launch_bounds__(kMain) void ssdb_carry_kernel(const SbArgs a) {
 }
 
 // What lies in LDS for a head of the main kernel: x of the tiles up to the own one and dy of those from it on; R; tables:
-// decays to the end of a token's tile, with delta, and from the end of the tile before it, delta, and the running sums. For
-// bfloat16 io twice: one head's is filled while the other's is read, with one barrier to a head.
+// decays to the end of a token's tile, with delta, and from the end of the tile before it, delta, and the running sums; and
+// what the waves that make dC have of dx. For bfloat16 io all but R and the latter twice: one head's is filled while the
+// other's is read.
 struct MainTables {
   double cs[kQ];
   float to_end[kQ], from_end[kQ], delta[kQ];
@@ -625,11 +653,12 @@ template <int IO, int N>
 struct MainLds {
   static constexpr int kBufs = IO == 1 ? 2 : 1, kSlots = kTiles + 1;
   static constexpr uint32_t kX = Lds<IO, kP>::kBytes, kState = LdsState<IO, N, 2>::kBytes;
-  static constexpr uint32_t kR = kBufs * kSlots * kX, kTab = kR + kBufs * kState,
+  static constexpr uint32_t kR = kBufs * kSlots * kX, kDx = kR + kState, kCol = kDx + kTile * kP * 4, kTab = kCol + 256 * 4,
                             kBytes = kTab + kBufs * static_cast<uint32_t>(sizeof(MainTables));
-  // before and behind the heads, B and C of a tile stand in the places of these
-  static constexpr uint32_t kB = kR, kC = 0;
-  static_assert(Lds<IO, N>::kBytes <= kR && Lds<IO, N>::kBytes <= kBufs * kState && kBytes <= 160 * 1024, "LDS");
+  // before and behind the heads, B and C of a tile stand in the places of these; behind them, what the waves that make dC
+  // have of dB
+  static constexpr uint32_t kB = kR, kC = 0, kDB = 0;
+  static_assert(Lds<IO, N>::kBytes <= kR && Lds<IO, N>::kBytes <= kState && kTile * N * 4 <= kR && kBytes <= 160 * 1024, "LDS");
 };
 struct MainPlace {
   int i, ntiles, valid, h0, h1, hs, grp, b, c;
@@ -684,7 +713,7 @@ struct MainFill {
         if (!whole && (slot <= pl.i ? slot : slot - 1) * kTile + row >= pl.valid) o = u4{0, 0, 0, 0};
         *reinterpret_cast<u4*>(lds + (buf * M::kSlots + slot) * M::kX + LX::at(row, i % LX::kPer * 16)) = o;
       }
-    r.template store<2>(lds + M::kR + buf * M::kState, tid);
+    r.template store<2>(lds + M::kR, tid);
     if (tid < kQ) {
       MainTables& tab = reinterpret_cast<MainTables*>(lds + M::kTab)[buf];
       tab.cs[tid] = cs;
@@ -697,16 +726,19 @@ struct MainFill {
 };
 
 // One task of the main kernel: dC of 16 tokens (MAKES_C), or dB and dx of them, which meet FAR tiles beside their own. The
-// other waves do the other task; they meet at the same barriers. The task that meets fewer tiles has registers left, and
-// fetches the next head for both (LOADS). A token is a lane's column throughout.
-template <int IO, int N, bool SEQ, bool MAKES_C, int FAR, bool LOADS>
+// other waves do the other task; they meet at the same barriers. The former also have what R has of dx, which the latter
+// take over at the second barrier of a head. With HELP, of the first of four tiles, which the two meet one and four
+// others of, they have the farthest tile's part of dB and dx too. The task with registers left fetches the next head for
+// both (LOADS). A token is a lane's column throughout.
+template <int IO, int N, bool SEQ, bool MAKES_C, int FAR, bool LOADS, bool HELP>
 __device__ __forceinline__ void ssdb_task(const SbArgs& a, const MainPlace& pl, char* lds) {
   using T = typename Io<IO>::T;
   using LX = Lds<IO, kP>;
   using LB = Lds<IO, N>;
   using LS = LdsState<IO, N, 2>;
   using M = MainLds<IO, N>;
-  constexpr int kNt = N / 16, kNb = N / 32, kHalf = kMain / 2;
+  constexpr int kNt = N / 16, kNb = N / 32, kHalf = kMain / 2, kLast = kTiles - 1;
+  constexpr bool kHelps = HELP && MAKES_C;
   const int tid = threadIdx.x, lane = tid & 63, l15 = lane & 15, g = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6) & 3;
   const int i = pl.i, ntiles = pl.ntiles, valid = pl.valid;
@@ -716,8 +748,11 @@ __device__ __forceinline__ void ssdb_task(const SbArgs& a, const MainPlace& pl, 
   const T* Cg = static_cast<const T*>(a.C) + row0 * a.c_row + pl.grp * N;
   const int own = i * kTile + 16 * w + l15;  // the lane's token in the chunk
   const bool live = own < valid;
-  int bound = MAKES_C ? 0 : kQ;  // the tokens that it meets begin or end here
-  if (SEQ) bound = (MAKES_C ? a.begin : a.next)[bc * kQ + own];
+  int begin = 0, next = kQ;  // the tokens that it meets begin, and end, here
+  if (SEQ) {
+    begin = a.begin[bc * kQ + own];
+    next = a.next[bc * kQ + own];
+  }
   auto rows_in = [&](int k) { return min(kTile, valid - k * kTile); };
   // a place in a loop from which on what follows from the lane's numbers is worked out anew: kept over the loop, it
   // would cost the registers that the sums need
@@ -730,53 +765,78 @@ __device__ __forceinline__ void ssdb_task(const SbArgs& a, const MainPlace& pl, 
     const Frag<IO> f = frag8(base + (live ? own : 0) * ld + 32 * kb + 8 * g);
     return live ? f : frag_zero<IO>();
   };
-  // B of tile i - d and C of tile i + d, where there are such
-  auto fill_bc = [&](int d) {
+  // B of tile i - d and C of tile i + d, where there are such, one after the other: f(d) multiplies them
+  auto all_bc = [&](auto&& f) {
+    typename LB::template Way<kMain> wb, wc;
+    auto fetch = [&](int d, int t) {
+      if (i - d >= 0) wb.load(Bg + (i - d) * kTile * a.b_row, a.b_row, 0, rows_in(i - d), t);
+      if (i + d < ntiles) wc.load(Cg + (i + d) * kTile * a.c_row, a.c_row, 0, rows_in(i + d), t);
+    };
     int t = tid;
     asm volatile("" : "+v"(t));
-    __syncthreads();
-    if (i - d >= 0) LB::template fill<kMain>(lds + M::kB, Bg + (i - d) * kTile * a.b_row, a.b_row, 0, rows_in(i - d), t);
-    if (i + d < ntiles) LB::template fill<kMain>(lds + M::kC, Cg + (i + d) * kTile * a.c_row, a.c_row, 0, rows_in(i + d), t);
+    fetch(0, t);
+#pragma unroll
+    for (int d = 0; d < kTiles; ++d) {
+      __syncthreads();
+      if (i - d >= 0) wb.store(lds + M::kB, t);
+      if (i + d < ntiles) wc.store(lds + M::kC, t);
+      __syncthreads();
+      if (d < kLast) fetch(d + 1, t);
+      f(d);
+    }
     __syncthreads();
   };
   const char* const theirs = lds + (MAKES_C ? M::kB : M::kC);
 
+  // a loader is half of the waves, or, with one buffer, all of them
+  constexpr int kLoaders = M::kBufs == 2 ? kHalf : kMain;
+  MainFill<IO, N, kLoaders> fill;
+  const int lt = M::kBufs == 2 ? tid & (kHalf - 1) : tid;
+  if (M::kBufs == 2 && LOADS) fill.load(a, pl, pl.h0, lt);
+
   // The own tile's tokens meet those of the tiles d = 0, 1, .. before it (dC) or behind it (dB, dx): of the first, the own
-  // one, those up to the token (from it on). C . B of each, for all heads, and the sums over the heads.
-  float G[FAR + 1][4][4], P[FAR + 1][4][4];
-  Frag<IO> f[kNb];  // the own row of C (B)
+  // one, those up to the token (from it on). C . B of each, for all heads, and the sums over the heads. (Gh, Ph: of the
+  // last tile behind it, for the other task.)
+  float G[FAR + 1][4][4], P[FAR + 1][4][4], Gh[kHelps ? 4 : 1][4], Ph[kHelps ? 4 : 1][4];
+  Frag<IO> bf[kNb];  // the own row of B
 #pragma unroll
-  for (int kb = 0; kb < kNb; ++kb) f[kb] = own_frag(MAKES_C ? Cg : Bg, MAKES_C ? a.c_row : a.b_row, kb);
+  for (int kb = 0; kb < kNb; ++kb) bf[kb] = own_frag(Bg, a.b_row, kb);
   {
+    Frag<IO> cf[MAKES_C ? kNb : 1];
+    if constexpr (MAKES_C)
 #pragma unroll
-    for (int d = 0; d < kTiles; ++d) {
-      fill_bc(d);
-      if (d > FAR) continue;
+      for (int kb = 0; kb < kNb; ++kb) cf[kb] = own_frag(Cg, a.c_row, kb);
+    all_bc([&](int d) {
       int l = l15, gg = g;
       renew(l, gg);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         f4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (d <= FAR) {
 #pragma unroll
-        for (int kb = 0; kb < kNb; ++kb) v = mma(LB::row(theirs, 16 * q, 32 * kb, l, gg), f[kb], v);
+          for (int kb = 0; kb < kNb; ++kb)
+            v = mma(LB::row(theirs, 16 * q, 32 * kb, l, gg), MAKES_C ? cf[MAKES_C ? kb : 0] : bf[kb], v);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          G[d <= FAR ? d : 0][q][j] = v[j];
-          P[d <= FAR ? d : 0][q][j] = 0.0f;
+          for (int j = 0; j < 4; ++j) {
+            G[d <= FAR ? d : 0][q][j] = v[j];
+            P[d <= FAR ? d : 0][q][j] = 0.0f;
+          }
+        }
+        if (kHelps && d == kLast) {
+          v = f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int kb = 0; kb < kNb; ++kb) v = mma(LB::row(lds + M::kC, 16 * q, 32 * kb, l, gg), bf[kb], v);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            Gh[kHelps ? q : 0][j] = v[j];
+            Ph[kHelps ? q : 0][j] = 0.0f;
+          }
         }
       }
-    }
+    });
   }
-  __syncthreads();  // B and C have been read
+  if (M::kBufs == 2 && LOADS) fill.store(pl, lds, 0, lt);
 
-  // a loader is half of the waves, or, with one buffer, all of them
-  constexpr int kLoaders = M::kBufs == 2 ? kHalf : kMain;
-  MainFill<IO, N, kLoaders> next;
-  const int lt = M::kBufs == 2 ? tid & (kHalf - 1) : tid;
-  if (M::kBufs == 2 && LOADS) {
-    next.load(a, pl, pl.h0, lt);
-    next.store(pl, lds, 0, lt);
-  }
   int buf = 0;
 #pragma unroll 1
   for (int h = pl.h0; h < pl.h1; ++h) {
@@ -784,108 +844,168 @@ __device__ __forceinline__ void ssdb_task(const SbArgs& a, const MainPlace& pl, 
     int t = lt, l = l15, gg = g;
     asm volatile("" : "+v"(t));
     renew(l, gg);
+    __syncthreads();  // this head's tiles are whole, or (one buffer) the last one's have been read
     if constexpr (M::kBufs == 2) {
-      __syncthreads();  // this head's buffer is whole, the other one has been read
-      if (LOADS) next.load(a, pl, min(h + 1, pl.h1 - 1), t);
+      if (LOADS) fill.load(a, pl, min(h + 1, pl.h1 - 1), t);
     } else {
-      __syncthreads();
-      next.load(a, pl, h, t);
-      next.store(pl, lds, 0, t);
+      fill.load(a, pl, h, t);
+      fill.store(pl, lds, 0, t);
       __syncthreads();
     }
     const MainTables& tab = reinterpret_cast<const MainTables*>(lds + M::kTab)[buf];
     const char* const toks = lds + buf * (M::kSlots * M::kX);
-    const char* const sR = lds + M::kR + buf * M::kState;
     const int me = i * kTile + 16 * w + l;  // the lane's token again
     const double cs_me = tab.cs[me];
     const char* const xi = toks + i * M::kX;
     const char* const yi = toks + (i + 1) * M::kX;
-
+    f4* const dx_in = reinterpret_cast<f4*>(lds + M::kDx) + w * 256 + lane;  // of the lane's token, as accumulators lie
+    float* const col_in = reinterpret_cast<float*>(lds + M::kCol) + w * 64 + lane;
+    const float delta = tab.delta[me];
     Frag<IO> mine[2];  // the own row of dy (x)
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) mine[kb] = LX::row(MAKES_C ? yi : xi, 16 * w, 32 * kb, l, gg);
-    const float delta = tab.delta[me];
-    f4 dx[MAKES_C ? 1 : 4];  // without delta and D: rows p = 16 pt + 4 g + j
-    if constexpr (!MAKES_C) {  // what comes from the gradient behind the chunk
-      const bool open = !SEQ || bound >= kQ;
-      const float e = decayed(tab.cs[kQ - 1] - cs_me);
+    f4 dx[4];  // without delta and D: rows p = 16 pt + 4 g + j
 #pragma unroll
-      for (int pt = 0; pt < 4; ++pt) dx[pt] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int pt = 0; pt < 4; ++pt) dx[pt] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+    // dy . x of 32 others and the lane's token: rows of the others
+    auto scores = [&](const char* other, int half, const Frag<IO>(&row)[2], f4(&m)[2]) {
+#pragma unroll
+      for (int o = 0; o < 2; ++o) {
+        m[o] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) m[o] = mma(LX::row(other, 32 * half + 16 * o, 32 * kb, l, gg), row[kb], m[o]);
+      }
+    };
+    // what 32 others have of dx: their dy times C . B, weighted
+    auto add_dx = [&](const char* other, int half, const f4(&gw)[2]) {
+      const Wide<IO, 2> v = wide<IO, 2>(gw[0], gw[1]);
+#pragma unroll
+      for (int pt = 0; pt < 4; ++pt) dx[pt] = mma_wide(LX::col_acc(other, 32 * half, 16 * pt, l, gg), v, dx[pt]);
+    };
+    // a half of tile i + d, d > 0, and the lane's token: its part of P, of the column of m (without delta) and of dx
+    auto behind = [&](int d, int half, const Frag<IO>(&row)[2], float (*Gd)[4], float (*Pd)[4], float& column) {
+      const int k = i + d;
+      const char* const other = toks + (k + 1) * M::kX;
+      const float er = decayed(tab.cs[k * kTile - 1] - cs_me);
+      f4 m[2], gw[2];
+      scores(other, half, row, m);
+#pragma unroll
+      for (int o = 0; o < 2; ++o) {
+        const int q = 2 * half + o, at = k * kTile + 16 * q + 4 * gg;
+        const f4 wt = *reinterpret_cast<const f4*>(tab.from_end + at) * er;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bool keep = !SEQ || at + j < next;
+          const float cb = keep ? Gd[q][j] : 0.0f, mw = keep ? m[o][j] * wt[j] : 0.0f;
+          gw[o][j] = cb * wt[j];
+          column = fmaf(mw, cb, column);
+          Pd[q][j] = fmaf(mw, delta, Pd[q][j]);
+        }
+      }
+      add_dx(other, half, gw);
+      // summed here, not where the sums are used: the terms would wait in registers
+#pragma unroll
+      for (int q = 2 * half; q < 2 * half + 2; ++q)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(column), "+v"(Pd[q][j]));
+    };
+    // the own tile: a place of m has the same bits in its row and in its column, of which the step kernel takes one from
+    // the other
+    float in = 0.0f, all = 0.0f, skip = 0.0f;
+    auto inside = [&](int half) {
+      f4 m[2], gw[2];
+      scores(MAKES_C ? xi : yi, half, mine, m);
+#pragma unroll
+      for (int o = 0; o < 2; ++o) {
+        const int q = 2 * half + o, at = i * kTile + 16 * q + 4 * gg;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int s = at + j;
+          const float wt = decayed(MAKES_C ? cs_me - tab.cs[s] : tab.cs[s] - cs_me), dl = MAKES_C ? tab.delta[s] : delta;
+          const bool keep = MAKES_C ? s <= me && (!SEQ || s >= begin) : s >= me && (!SEQ || s < next);
+          const float cb = keep ? G[0][q][j] : 0.0f, mw = keep ? m[o][j] * wt : 0.0f, mg = mw * cb;
+          in = fmaf(s == me ? 0.0f : mg, dl, in);
+          P[0][q][j] = fmaf(mw, dl, P[0][q][j]);
+          if (!MAKES_C) {
+            skip = s == me ? m[o][j] : skip;
+            all += mg;
+            gw[o][j] = cb * wt;
+          }
+        }
+      }
+      if (!MAKES_C) add_dx(yi, half, gw);
+#pragma unroll
+      for (int q = 2 * half; q < 2 * half + 2; ++q)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(in), "+v"(all), "+v"(P[0][q][j]));
+    };
+    float* const tok = a.tok + bch * kQ + me;
+
+    if constexpr (MAKES_C) {
+      // what comes from the gradient behind the chunk, for the other task
+      const bool open = !SEQ || next >= kQ;
+      const float e = decayed(tab.cs[kQ - 1] - cs_me);
 #pragma unroll
       for (int kb = 0; kb < kNb; ++kb) {
         if (IO == 0) renew(l, gg);
 #pragma unroll
-        for (int pt = 0; pt < 4; ++pt) dx[pt] = mma_wide(LS::row(sR, 16 * pt, 32 * kb, l, gg), f[kb], dx[pt]);
+        for (int pt = 0; pt < 4; ++pt) dx[pt] = mma_wide(LS::row(lds + M::kR, 16 * pt, 32 * kb, l, gg), bf[kb], dx[pt]);
       }
 #pragma unroll
       for (int pt = 0; pt < 4; ++pt)
 #pragma unroll
         for (int j = 0; j < 4; ++j) dx[pt][j] = open ? dx[pt][j] * e : 0.0f;
-    }
-    // The token's row (column) of m inside its tile and beyond it; x . dx without delta and D; dy . x. A place of m has
-    // the same bits in its row and in its column: the step kernel takes one from the other.
-    float in = 0.0f, out[MAKES_C ? FAR + 1 : 2] = {}, skip = 0.0f, corner = 0.0f;
+      if constexpr (kHelps) {
+        Frag<IO> row[2];  // the own row of x
 #pragma unroll
-    for (int d = 0; d <= FAR; ++d) {
-      const int k = MAKES_C ? i - d : i + d;
-      const char* const other = toks + (MAKES_C ? k : k + 1) * M::kX;  // x (dy) of it
-      const float er = d == 0 ? 0.0f : decayed(MAKES_C ? cs_me - tab.cs[k * kTile + kTile - 1] : tab.cs[k * kTile - 1] - cs_me);
+        for (int kb = 0; kb < 2; ++kb) row[kb] = LX::row(xi, 16 * w, 32 * kb, l, gg);
+        float column = 0.0f;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          renew(l, gg);
+          behind(kLast, half, row, Gh, Ph, column);
+        }
+        *col_in = column;
+      }
+#pragma unroll
+      for (int pt = 0; pt < 4; ++pt) dx_in[64 * pt] = dx[pt];
+      __syncthreads();  // the other task's, and R has been read
+      float out[FAR + 1] = {};
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        f4 gw[2];
         renew(l, gg);
+        inside(half);
+      }
 #pragma unroll
-        for (int o = 0; o < 2; ++o) {
-          const int q = 2 * half + o, at = k * kTile + 16 * q + 4 * gg;
-          f4 m = {0.0f, 0.0f, 0.0f, 0.0f}, wt;  // dy . x: rows of the others, the lane's token
+      for (int d = 1; d <= FAR; ++d) {
+        const int k = i - d;
+        const char* const other = toks + k * M::kX;
+        const float er = decayed(cs_me - tab.cs[k * kTile + kTile - 1]);
 #pragma unroll
-          for (int kb = 0; kb < 2; ++kb) m = mma(LX::row(other, 16 * q, 32 * kb, l, gg), mine[kb], m);
-          if (d > 0) {
-            wt = *reinterpret_cast<const f4*>((MAKES_C ? tab.to_end : tab.from_end) + at) * er;
-          } else {
+        for (int half = 0; half < 2; ++half) {
+          renew(l, gg);
+          f4 m[2];
+          scores(other, half, mine, m);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) wt[j] = decayed(MAKES_C ? cs_me - tab.cs[at + j] : tab.cs[at + j] - cs_me);
-          }
+          for (int o = 0; o < 2; ++o) {
+            const int q = 2 * half + o, at = k * kTile + 16 * q + 4 * gg;
+            const f4 wt = *reinterpret_cast<const f4*>(tab.to_end + at) * er;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int s = at + j;
-            const bool all = d > 0 && !SEQ;
-            const bool keep = MAKES_C ? (d > 0 || s <= me) && (!SEQ || s >= bound) : (d > 0 || s >= me) && (!SEQ || s < bound);
-            const float cb = all || keep ? G[d][q][j] : 0.0f;
-            if (!MAKES_C && d == 0) skip = s == me ? m[j] : skip;
-            const float mw = all || keep ? m[j] * wt[j] : 0.0f;
-            if (!MAKES_C) gw[o][j] = cb * wt[j];
-            if (d == 0) {
-              const float mg = mw * cb, dl = MAKES_C ? tab.delta[s] : delta;
-              if (!MAKES_C) corner = s == me ? mg : corner;
-              in = fmaf(s == me ? 0.0f : mg, dl, in);
-              if (!MAKES_C) out[0] += mg;
-              P[d][q][j] = fmaf(mw, dl, P[d][q][j]);
-            } else if (MAKES_C) {
-              out[d] = fmaf(mw, cb, out[d]);
+            for (int j = 0; j < 4; ++j) {
+              const bool keep = !SEQ || at + j >= begin;
+              const float mw = keep ? m[o][j] * wt[j] : 0.0f;
+              out[d] = fmaf(mw, keep ? G[d][q][j] : 0.0f, out[d]);
               P[d][q][j] += mw;
-            } else {
-              out[1] = fmaf(mw, cb, out[1]);
-              P[d][q][j] = fmaf(mw, delta, P[d][q][j]);
             }
           }
+#pragma unroll
+          for (int q = 2 * half; q < 2 * half + 2; ++q)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(out[d]), "+v"(P[d][q][j]));
         }
-        if constexpr (!MAKES_C) {
-          const Wide<IO, 2> v = wide<IO, 2>(gw[0], gw[1]);
-#pragma unroll
-          for (int pt = 0; pt < 4; ++pt) dx[pt] = mma_wide(LX::col_acc(other, 32 * half, 16 * pt, l, gg), v, dx[pt]);
-        }
-        // summed here, not where the sums are used: the terms would wait in registers
-#pragma unroll
-        for (int q = 2 * half; q < 2 * half + 2; ++q)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(in), "+v"(out[MAKES_C ? d : d > 0]), "+v"(P[d][q][j]));
       }
-    }
-    renew(l, gg);
-    float* const tok = a.tok + bch * kQ + me;
-    in = over_g(in);
-    if constexpr (MAKES_C) {
+      renew(l, gg);
+      in = over_g(in);
       if (gg == 0) tok[kRowIn * a.tok_step] = in;
 #pragma unroll
       for (int d = 1; d <= FAR; ++d) {
@@ -893,17 +1013,40 @@ __device__ __forceinline__ void ssdb_task(const SbArgs& a, const MainPlace& pl, 
         if (gg == 0) tok[(kRow1 + d - 1) * a.tok_step] = out[d];
       }
     } else {
-      out[0] = over_g(out[0]);
-      out[1] = over_g(out[1]);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        renew(l, gg);
+        inside(half);
+      }
+      float column = 0.0f;
+      auto whole_behind = [&](int d) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          renew(l, gg);
+          behind(d, half, mine, G[d], P[d], column);
+        }
+      };
+      // a task that helps is there later
+      constexpr int kBefore = HELP ? 1 : 0;
+#pragma unroll
+      for (int d = 1; d <= kBefore; ++d) whole_behind(d);
+      __syncthreads();  // the other task has its part of dx
+#pragma unroll
+      for (int d = kBefore + 1; d <= FAR; ++d) whole_behind(d);
+      renew(l, gg);
+      if (HELP) column += *col_in;
+      in = over_g(in);
+      all = over_g(all);
+      column = over_g(column);
       skip = over_g(skip);  // one lane has it
       const float D = tab.D;
       T* to = static_cast<T*>(a.dx) + ((row0 + me) * a.nheads + h) * kP + 4 * gg;
 #pragma unroll
       for (int pt = 0; pt < 4; ++pt) {
-        const f4 yv = LX::four(yi, 16 * w + l, 16 * pt + 4 * gg);
+        const f4 yv = LX::four(yi, 16 * w + l, 16 * pt + 4 * gg), more = dx_in[64 * pt];
         f4 v;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = fmaf(delta, dx[pt][j], D * yv[j]);
+        for (int j = 0; j < 4; ++j) v[j] = fmaf(delta, dx[pt][j] + more[j], D * yv[j]);
         if (me < valid) {
           if constexpr (IO == 1) {
             *reinterpret_cast<u2*>(to + 16 * pt) = u2{round2(v[0], v[1]), round2(v[2], v[3])};
@@ -914,45 +1057,64 @@ __device__ __forceinline__ void ssdb_task(const SbArgs& a, const MainPlace& pl, 
       }
       if (gg == 0) {
         tok[kColIn * a.tok_step] = in;
-        tok[kColOut * a.tok_step] = delta * out[1];
-        tok[kDirect * a.tok_step] = out[0] + out[1];
+        tok[kColOut * a.tok_step] = delta * column;
+        tok[kDirect * a.tok_step] = all + column;
         tok[kSkip * a.tok_step] = skip;
       }
     }
     if constexpr (M::kBufs == 2) {
-      if (LOADS) next.store(pl, lds, buf ^ 1, t);
+      if (LOADS) fill.store(pl, lds, buf ^ 1, t);
       buf ^= 1;
     }
   }
 
-  // the sums over the heads meet B and C
+  // the sums over the heads meet B and C, beside what the states carry
+  const int64_t at = ((row0 + (live ? own : 0)) * a.ngroups + pl.grp) * N + 4 * g, whole = static_cast<int64_t>(a.batch) * a.seqlen * a.ngroups * N;
   f4 out[kNt];  // dC^T or dB^T: rows n = 16 nt + 4 g + j, the lane's token
 #pragma unroll
   for (int nt = 0; nt < kNt; ++nt) out[nt] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+  if (pl.hs == 0)
+    for (int k = 0; k < a.csplit; ++k) {
+      const float* from = (MAKES_C ? a.dCc : a.dBc) + k * whole + at;
 #pragma unroll
-  for (int d = 0; d < kTiles; ++d) {
-    fill_bc(d);
-    if (d > FAR) continue;
+      for (int nt = 0; nt < kNt; ++nt) out[nt] += *reinterpret_cast<const f4*>(from + 16 * nt);
+    }
+  f4 help[kHelps ? kNt : 1];
+  auto times = [&](const char* tile, const float (*Pd)[4], f4* to) {
     int l = l15, gg = g;
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       renew(l, gg);
-      const float(&lo)[4] = P[d <= FAR ? d : 0][2 * m], (&hi)[4] = P[d <= FAR ? d : 0][2 * m + 1];
+      const float(&lo)[4] = Pd[2 * m], (&hi)[4] = Pd[2 * m + 1];
       const Wide<IO, 2> v = wide<IO, 2>(f4{lo[0], lo[1], lo[2], lo[3]}, f4{hi[0], hi[1], hi[2], hi[3]});
 #pragma unroll
-      for (int nt = 0; nt < kNt; ++nt) out[nt] = mma_wide(LB::col_acc(theirs, 32 * m, 16 * nt, l, gg), v, out[nt]);
+      for (int nt = 0; nt < kNt; ++nt) to[nt] = mma_wide(LB::col_acc(tile, 32 * m, 16 * nt, l, gg), v, to[nt]);
+    }
+  };
+  all_bc([&](int d) {
+    if (d <= FAR) times(theirs, P[d <= FAR ? d : 0], out);
+    if constexpr (kHelps)
+      if (d == kLast) {
+#pragma unroll
+        for (int nt = 0; nt < kNt; ++nt) help[nt] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+        times(lds + M::kC, Ph, help);
+      }
+  });
+  if constexpr (HELP) {
+    f4* const db = reinterpret_cast<f4*>(lds + M::kDB) + w * (64 * kNt) + lane;
+    if constexpr (kHelps) {
+#pragma unroll
+      for (int nt = 0; nt < kNt; ++nt) db[64 * nt] = help[nt];
+    }
+    __syncthreads();
+    if constexpr (!MAKES_C) {
+#pragma unroll
+      for (int nt = 0; nt < kNt; ++nt) out[nt] += db[64 * nt];
     }
   }
   if (!live) return;
-  const int64_t at = ((row0 + own) * a.ngroups + pl.grp) * N + 4 * g, all = static_cast<int64_t>(a.batch) * a.seqlen * a.ngroups * N;
-  if (pl.hs == 0)  // and what the states carry
-    for (int k = 0; k < a.csplit; ++k) {
-      const float* from = (MAKES_C ? a.dCc : a.dBc) + k * all + at;
-#pragma unroll
-      for (int nt = 0; nt < kNt; ++nt) out[nt] += *reinterpret_cast<const f4*>(from + 16 * nt);
-    }
   if (a.hsplit > 1) {
-    float* to = (MAKES_C ? a.dCp : a.dBp) + pl.hs * all + at;
+    float* to = (MAKES_C ? a.dCp : a.dBp) + pl.hs * whole + at;
 #pragma unroll
     for (int nt = 0; nt < kNt; ++nt) *reinterpret_cast<f4*>(to + 16 * nt) = out[nt];
     return;
@@ -995,21 +1157,22 @@ __global__ __launch_bounds__(kMain) void ssdb_main_kernel(const SbArgs a) {
   pl.h0 = pl.grp * rep + pl.hs * a.per;
   pl.h1 = min(pl.h0 + a.per, (pl.grp + 1) * rep);
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+  const int far = pl.ntiles - 1 - pl.i;
   if (wave < 4) {
+    if (IO == 1 && far == 3) return ssdb_task<IO, N, SEQ, true, 0, true, IO == 1>(a, pl, lds);
     switch (pl.i) {
-      case 0: return ssdb_task<IO, N, SEQ, true, 0, true>(a, pl, lds);
-      case 1: return ssdb_task<IO, N, SEQ, true, 1, true>(a, pl, lds);
-      case 2: return ssdb_task<IO, N, SEQ, true, 2, true>(a, pl, lds);
-      default: return ssdb_task<IO, N, SEQ, true, 3, false>(a, pl, lds);
+      case 0: return ssdb_task<IO, N, SEQ, true, 0, true, false>(a, pl, lds);
+      case 1: return ssdb_task<IO, N, SEQ, true, 1, true, false>(a, pl, lds);
+      case 2: return ssdb_task<IO, N, SEQ, true, 2, true, false>(a, pl, lds);
+      default: return ssdb_task<IO, N, SEQ, true, 3, false, false>(a, pl, lds);
     }
   }
-  const int far = pl.ntiles - 1 - pl.i;
-  if (IO == 1 && pl.i == 3) return ssdb_task<IO, N, SEQ, false, 0, true>(a, pl, lds);
+  if (IO == 1 && pl.i == 3) return ssdb_task<IO, N, SEQ, false, 0, true, false>(a, pl, lds);
   switch (far) {
-    case 0: return ssdb_task<IO, N, SEQ, false, 0, false>(a, pl, lds);
-    case 1: return ssdb_task<IO, N, SEQ, false, 1, false>(a, pl, lds);
-    case 2: return ssdb_task<IO, N, SEQ, false, 2, false>(a, pl, lds);
-    default: return ssdb_task<IO, N, SEQ, false, 3, false>(a, pl, lds);
+    case 0: return ssdb_task<IO, N, SEQ, false, 0, false, false>(a, pl, lds);
+    case 1: return ssdb_task<IO, N, SEQ, false, 1, false, false>(a, pl, lds);
+    case 2: return ssdb_task<IO, N, SEQ, false, 2, false, false>(a, pl, lds);
+    default: return ssdb_task<IO, N, SEQ, false, IO == 1 ? 2 : 3, false, IO == 1>(a, pl, lds);
   }
 }
 
@@ -1072,7 +1235,7 @@ __global__ __launch_bounds__(kQ) void ssdb_step_kernel(const SbArgs a) {
   const float decay = a.decay[bch];
   if (decay != 0.0f) {
     double whole = 0.0;
-    for (int i = 0; i < 8; ++i) whole += a.dot[bch * 8 + i];
+    for (int i = 0; i < 16; ++i) whole += a.dot[bch * 16 + i];
     g += whole * decay;
   }
   if (SEQ && a.begin[bc * kQ + tid] == tid) g = 0.0;  // nothing reaches a document's first token
@@ -1147,7 +1310,7 @@ Ws layout(int32_t batch, int32_t seqlen, int32_t nheads, int32_t d_state, int32_
   w.delta = take(bch * kQ * 4);
   w.begin = take(bc * kQ * 4);
   w.next = take(bc * kQ * 4);
-  w.dot = take(bch * 8 * 4);
+  w.dot = take(bch * 16 * 4);
   w.tok = take(bch * kQ * 4 * kTokSums);
   w.tok_step = bch * kQ;
   w.dBp = take(part);
