@@ -123,7 +123,7 @@ size_t mamba_conv_bwd_workspace_bytes(int32_t batch, int32_t seqlen, int32_t cha
   const std::string saved = last_error();
   const int st = check_dims(batch, seqlen, channels, taps, io_dtype);
   last_error() = saved;
-  return st ? 0 : mscan::conv_part_floats(batch, seqlen, channels, taps, io_dtype) * sizeof(float);
+  return st ? 0 : mscan::conv_part_floats(batch, seqlen, channels, taps) * sizeof(float);
 }
 
 int mamba_conv_bwd(int32_t batch, int32_t seqlen, int32_t channels, int32_t taps, int32_t io_dtype,
@@ -163,7 +163,7 @@ int mamba_conv_bwd(int32_t batch, int32_t seqlen, int32_t channels, int32_t taps
   for (const void* p : {static_cast<const void*>(dstate_out), static_cast<const void*>(dweight),
                         static_cast<const void*>(dbias), static_cast<const void*>(dstate_in)})
     if (!aligned(p, 4)) return fail(MAMBA_ERR_ALIGN, "float32 pointers must be 4-byte aligned");
-  const size_t need = mscan::conv_part_floats(batch, seqlen, channels, taps, io_dtype) * sizeof(float);
+  const size_t need = mscan::conv_part_floats(batch, seqlen, channels, taps) * sizeof(float);
   Range ins[6 + MAMBA_CONV_MAX_PARTS] = {
       rows_range("x", x, rows, x_stride, channels, es), range("seq_idx", seq_idx, rows * 4),
       range("weight", weight, par * taps), range("bias", bias, par), range("state_in", state_in, state_bytes(c)),

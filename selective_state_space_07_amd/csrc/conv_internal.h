@@ -29,7 +29,7 @@ struct ConvCall {
   hipStream_t stream;
 };
 // Workspace floats of a backward call.
-size_t conv_part_floats(int32_t batch, int32_t seqlen, int32_t channels, int32_t taps, int32_t io_dtype);
+size_t conv_part_floats(int32_t batch, int32_t seqlen, int32_t channels, int32_t taps);
 hipError_t launch_conv(const ConvCall& c);
 hipError_t launch_conv_step(const ConvCall& c);
 
