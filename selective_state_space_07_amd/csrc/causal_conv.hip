@@ -504,7 +504,7 @@ hipError_t launch_taps(const ConvCall& c, ConvArgs a) {
     hipLaunchKernelGGL((conv_bwd_kernel<IO, V, K, false>), grid, block, 0, c.stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return launch_part_sums(s.nblk, c.channels * K, a.pw, c.dweight, c.channels, a.pb, c.dbias, c.stream);
+  return launch_part_sums(s.nblk, {{c.channels * K, a.pw, c.dweight}, {c.channels, a.pb, c.dbias}}, c.stream);
 }
 
 template <int IO, int V>

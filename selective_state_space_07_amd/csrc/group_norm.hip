@@ -589,7 +589,7 @@ hipError_t launch_gnorm(const GnCall& c) {
   a.pb = c.dbias ? c.part + (c.dweight ? n : 0) : nullptr;
   hipError_t e = c.io_dtype == 0 ? launch_io<0>(c, l, a) : launch_io<1>(c, l, a);
   if (e != hipSuccess || (!a.pw && !a.pb)) return e;
-  return launch_part_sums(a.nblk, c.channels, a.pw, c.dweight, c.channels, a.pb, c.dbias, c.stream);
+  return launch_part_sums(a.nblk, {{c.channels, a.pw, c.dweight}, {c.channels, a.pb, c.dbias}}, c.stream);
 }
 
 }  // namespace mscan

@@ -465,7 +465,7 @@ hipError_t launch_rmsnorm(const RnCall& c) {
   else
     e = c.residual_dtype == 0 ? launch_io<1, 0>(c, l, a) : launch_io<1, 1>(c, l, a);
   if (e != hipSuccess || !a.pw) return e;
-  return launch_part_sums(a.nblk, c.channels, a.pw, c.dweight, 0, nullptr, nullptr, c.stream);
+  return launch_part_sums(a.nblk, {{c.channels, a.pw, c.dweight}}, c.stream);
 }
 
 }  // namespace mscan

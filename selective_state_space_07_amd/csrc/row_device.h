@@ -3,6 +3,8 @@
 // sum of the partial sums that workgroups leave of a parameter's gradient.
 #pragma once
 
+#include <initializer_list>
+
 #include "mfma_frag.h"
 #include "scan_device.h"
 
@@ -165,12 +167,17 @@ __device__ __forceinline__ float act_grad(int kind, float z, float& a) {
 
 // out[c] = sum over blocks of part[block][c]: 16 channels a workgroup, whose 64
 // quarter waves take every 64th block, four at a time.
-__global__ __launch_bounds__(1024) void part_sum_kernel(int32_t nblk, int32_t n0, const float* p0, float* o0,
-                                                        int32_t n1, const float* p1, float* o1) {
+struct PartSum {
+  int32_t n;  // channels
+  const float* part;
+  float* out;
+};
+__global__ __launch_bounds__(1024) void part_sum_kernel(int32_t nblk, PartSum s0, PartSum s1, PartSum s2) {
   __shared__ float red[64][17];
-  const float* part = blockIdx.y == 0 ? p0 : p1;
-  float* out = blockIdx.y == 0 ? o0 : o1;
-  const int32_t channels = blockIdx.y == 0 ? n0 : n1;
+  const PartSum set = blockIdx.y == 0 ? s0 : blockIdx.y == 1 ? s1 : s2;
+  const float* part = set.part;
+  float* out = set.out;
+  const int32_t channels = set.n;
   if (!out) return;
   const int l = threadIdx.x & 15, h = threadIdx.x >> 4;
   const int c = blockIdx.x * 16 + l;
@@ -191,12 +198,18 @@ __global__ __launch_bounds__(1024) void part_sum_kernel(int32_t nblk, int32_t n0
   }
 }
 
-// Both sums of a call in one launch; a set without an output is left out.
-hipError_t launch_part_sums(int32_t nblk, int32_t n0, const float* p0, float* o0, int32_t n1, const float* p1, float* o1,
-                            hipStream_t stream) {
-  const int32_t n = n0 > n1 ? n0 : n1;
-  hipLaunchKernelGGL(part_sum_kernel, dim3(static_cast<unsigned>((n + 15) / 16), 2), dim3(1024), 0, stream, nblk, n0, p0,
-                     o0, n1, p1, o1);
+// Up to three sums of a call in one launch; a set without an output is left out.
+hipError_t launch_part_sums(int32_t nblk, std::initializer_list<PartSum> sets, hipStream_t stream) {
+  PartSum s[3] = {};
+  int32_t n = 0, used = 0;
+  for (const PartSum& set : sets)
+    if (set.out) {
+      n = n > set.n ? n : set.n;
+      s[used++] = set;
+    }
+  if (!used) return hipSuccess;
+  hipLaunchKernelGGL(part_sum_kernel, dim3(static_cast<unsigned>((n + 15) / 16), static_cast<unsigned>(used)), dim3(1024), 0, stream,
+                     nblk, s[0], s[1], s[2]);
   return hipGetLastError();
 }
 

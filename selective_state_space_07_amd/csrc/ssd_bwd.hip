@@ -1278,14 +1278,24 @@ __global__ __launch_bounds__(256) void ssdb_join_kernel(int64_t n4, int32_t spli
   }
 }
 
-// Heads of a group are split over workgroups until each CU has one. (A chunk has kTiles of the main kernel, and two of
-// the carry kernel.)
-int heads_split(int32_t batch, int32_t nchunks, int32_t nheads, int32_t ngroups, int of_chunk) {
+// Workgroups that share the heads of a group: as many as end first. One takes a CU for itself, and a time of `fixed` heads
+// before and behind its own. (A chunk has kTiles of the main kernel, and two of the carry kernel. Twelve heads in three
+// groups, 2 x 1501 tokens, float32: split in two, which is 288 workgroups, the main kernel took 124 us, whole MAINFIG.)
+int heads_split(int32_t batch, int32_t nchunks, int32_t nheads, int32_t ngroups, int of_chunk, int fixed) {
   const int rep = nheads / ngroups;
   const int64_t units = static_cast<int64_t>(batch) * nchunks * ngroups * of_chunk;
-  int n = static_cast<int>(std::min<int64_t>(rep, (255 + units) / units));
-  const int per = (rep + n - 1) / n;
-  return (rep + per - 1) / per;
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int n = 1; n <= rep && (n == 1 || units * n <= 1024); ++n) {
+    const int per = (rep + n - 1) / n;
+    if ((rep + per - 1) / per != n) continue;
+    const int64_t time = (units * n + 255) / 256 * (fixed + per);
+    if (time < least) {
+      least = time;
+      best = n;
+    }
+  }
+  return best;
 }
 
 struct Ws {
@@ -1300,8 +1310,8 @@ Ws layout(int32_t batch, int32_t seqlen, int32_t nheads, int32_t d_state, int32_
     return here;
   };
   const size_t nchunks = (static_cast<size_t>(seqlen) + kQ - 1) / kQ, bc = batch * nchunks, bch = bc * nheads;
-  const size_t split = heads_split(batch, static_cast<int32_t>(nchunks), nheads, ngroups, kTiles);
-  const size_t csplit = heads_split(batch, static_cast<int32_t>(nchunks), nheads, ngroups, 2);
+  const size_t split = heads_split(batch, static_cast<int32_t>(nchunks), nheads, ngroups, kTiles, 4);
+  const size_t csplit = heads_split(batch, static_cast<int32_t>(nchunks), nheads, ngroups, 2, 2);
   const size_t one = static_cast<size_t>(batch) * seqlen * ngroups * static_cast<size_t>(d_state) * 4, part = split > 1 ? split * one : 0;
   w.S = take(bch * kP * d_state * 4);
   w.R = take(bch * kP * d_state * 4);
@@ -1342,8 +1352,8 @@ hipError_t launch_typed(const SsdBwdCall& c, const SbArgs& a) {
   hipLaunchKernelGGL((ssdb_step_kernel<IO, SEQ>), dim3(a.nchunks, a.nheads, a.batch), dim3(kQ), 0, c.stream, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const int nblk = a.batch * a.nchunks;
-  if ((e = launch_part_sums(nblk, a.nheads, a.pA, a.dA, a.nheads, a.pb, a.ddt_bias, c.stream)) != hipSuccess) return e;
-  if ((e = launch_part_sums(nblk, a.nheads, a.pD, a.dD, 0, nullptr, nullptr, c.stream)) != hipSuccess) return e;
+  if ((e = launch_part_sums(nblk, {{a.nheads, a.pA, a.dA}, {a.nheads, a.pb, a.ddt_bias}, {a.nheads, a.pD, a.dD}}, c.stream)) != hipSuccess)
+    return e;
   if (a.hsplit > 1) {
     using T = typename Io<IO>::T;
     const int64_t n4 = static_cast<int64_t>(a.batch) * a.seqlen * a.ngroups * N / 4;
@@ -1373,9 +1383,9 @@ hipError_t launch_ssd_bwd(const SsdBwdCall& c) {
   a.nheads = c.nheads;
   a.ngroups = c.ngroups;
   a.nchunks = (c.seqlen + kQ - 1) / kQ;
-  a.hsplit = heads_split(c.batch, a.nchunks, c.nheads, c.ngroups, kTiles);
+  a.hsplit = heads_split(c.batch, a.nchunks, c.nheads, c.ngroups, kTiles, 4);
   a.per = (c.nheads / c.ngroups + a.hsplit - 1) / a.hsplit;
-  a.csplit = heads_split(c.batch, a.nchunks, c.nheads, c.ngroups, 2);
+  a.csplit = heads_split(c.batch, a.nchunks, c.nheads, c.ngroups, 2, 2);
   a.cper = (c.nheads / c.ngroups + a.csplit - 1) / a.csplit;
   a.x_row = c.x_row;
   a.dt_row = c.dt_row;
