@@ -160,6 +160,7 @@ __device__ __forceinline__ uint32_t round2(float a, float b) {
 // Two values' parts as words of two bfloat16.
 template <int NP>
 __device__ __forceinline__ void parts2(float a, float b, uint32_t (&w)[NP]) {
+#pragma clang fp contract(off)  // the parts are of the rounded values, whatever made these
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
     w[p] = p == 0 && NP == 3 ? __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u) : round2(a, b);
@@ -263,7 +264,7 @@ struct StateWay {
 };
 
 struct SbArgs {
-  int32_t batch, seqlen, nheads, ngroups, nchunks;
+  int32_t batch, seqlen, nheads, ngroups, d_state, nchunks;
   int32_t hsplit, per, csplit, cper;  // workgroups that share a group's heads, and the heads of one: main and carry kernel
   int64_t x_row, dt_row, b_row, c_row, dy_row;
   const void *x, *dt, *B, *C, *dy;
@@ -286,7 +287,7 @@ struct SbArgs {
 };
 // What the step kernel has of each token: its row of m inside its tile (before the token) and over the three tiles before
 // it, nearest first; its column inside its tile and over the tiles behind it; its shares in g of S and, without delta, of
-// R; x . dx without delta and D, but for R's share; dy . x.
+// R, whether or not these reach it; x . dx without delta and D, but for R's share; dy . x.
 enum { kRowIn, kRow1, kRow2, kRow3, kColIn, kColOut, kOfS, kOfR, kDirect, kSkip, kTokSums };
 
 // exp of a difference of running sums, at most 0
@@ -304,6 +305,31 @@ __device__ __forceinline__ V scan256(V v, V* part, int tid, F f) {
   if (lane == 63) part[tid >> 6] = v;
   __syncthreads();
   for (int w = (tid >> 6) - 1; w >= 0; --w) v = f(part[w], v);
+  return v;
+}
+
+// A running sum over the threads that starts again where `restart` is; without one, of scan256's bits.
+__device__ __forceinline__ double scan256_runs(double v, bool restart, double* part, int* ipart, int tid) {
+  const int lane = tid & 63;
+  int cut = restart;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const double u = __shfl_up(v, o, 64);
+    const int c = __shfl_up(cut, o, 64);
+    if (lane >= o) {
+      if (!cut) v = u + v;
+      cut |= c;
+    }
+  }
+  if (lane == 63) {
+    part[tid >> 6] = v;
+    ipart[tid >> 6] = cut;
+  }
+  __syncthreads();
+  for (int w = (tid >> 6) - 1; w >= 0 && !cut; --w) {
+    v = part[w] + v;
+    cut = ipart[w];
+  }
   return v;
 }
 
@@ -328,14 +354,17 @@ __global__ __launch_bounds__(kState) void ssdb_state_kernel(const SbArgs a) {
 
   float delta = 0.0f;
   if (tid < valid) delta = softplus(Io<IO>::load(static_cast<const T*>(a.dt) + (row0 + tid) * a.dt_row + h) + a.dt_bias[h]);
-  const double cs = scan256(static_cast<double>(delta) * a.A[h], part, tid, [](double p, double q) { return p + q; });
+  // the running sum; a document's begin starts it again, so that what another holds is no part of it
+  bool restart = false;
+  if (SEQ) restart = tid < valid && static_cast<int64_t>(c) * kQ + tid > 0 && a.seq_idx[row0 + tid] != a.seq_idx[row0 + tid - 1];
+  double own = static_cast<double>(delta) * a.A[h];
+  asm volatile("" : "+v"(own));  // rounded here, and not with the first sum
+  const double cs = SEQ ? scan256_runs(own, restart, part, ipart, tid) : scan256(own, part, tid, [](double p, double q) { return p + q; });
+  if (SEQ) __syncthreads();
   if (tid == kQ - 1) cs_end = cs;
   int first = 0, last = valid;  // the tokens that count
   if (SEQ) {
-    const int64_t t = static_cast<int64_t>(c) * kQ + tid;
-    const int32_t* id = a.seq_idx + static_cast<int64_t>(b) * a.seqlen + t;
-    const bool starts = tid < valid && t > 0 && id[0] != id[-1];
-    const int begin = scan256(starts ? tid : -1, ipart, tid, [](int p, int q) { return p > q ? p : q; });
+    const int begin = scan256(restart ? tid : -1, ipart, tid, [](int p, int q) { return p > q ? p : q; });
     __syncthreads();
     // the first begin behind a token: a scan from the last one
     const bool mirror = kQ - 1 - tid < valid && static_cast<int64_t>(c) * kQ + kQ - 1 - tid > 0 &&
@@ -598,11 +627,11 @@ __device__ __forceinline__ void ssdb_carry(const SbArgs& a, int u, char* lds) {
         }
       }
     }
-    // a token that the state does not reach has sums of its own too, and none of them counts
+    // a token that the state does not reach has sums of its own too: of these none counts
 #pragma unroll
     for (int k = 0; k < kTok; ++k) {
       share[k] = over_g(share[k]) * e[k];
-      if (g == 0) a.tok[(OF_C ? kOfS : kOfR) * a.tok_step + bch * kQ + at[k]] = open[k] ? share[k] : 0.0f;
+      if (g == 0) a.tok[(OF_C ? kOfS : kOfR) * a.tok_step + bch * kQ + at[k]] = share[k];
     }
     if (from == 0) {
       float s = 0.0f;
@@ -897,7 +926,7 @@ __device__ __forceinline__ void ssdb_task(const SbArgs& a, const MainPlace& pl, 
         for (int j = 0; j < 4; ++j) {
           const bool keep = !SEQ || at + j < next;
           const float cb = keep ? Gd[q][j] : 0.0f, mw = keep ? m[o][j] * wt[j] : 0.0f;
-          gw[o][j] = cb * wt[j];
+          gw[o][j] = !SEQ || keep ? cb * wt[j] : 0.0f;
           column = fmaf(mw, cb, column);
           Pd[q][j] = fmaf(mw, delta, Pd[q][j]);
         }
@@ -921,15 +950,15 @@ __device__ __forceinline__ void ssdb_task(const SbArgs& a, const MainPlace& pl, 
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int s = at + j;
-          const float wt = decayed(MAKES_C ? cs_me - tab.cs[s] : tab.cs[s] - cs_me), dl = MAKES_C ? tab.delta[s] : delta;
+          const float wt = decayed(MAKES_C ? cs_me - tab.cs[s] : tab.cs[s] - cs_me);
           const bool keep = MAKES_C ? s <= me && (!SEQ || s >= begin) : s >= me && (!SEQ || s < next);
-          const float cb = keep ? G[0][q][j] : 0.0f, mw = keep ? m[o][j] * wt : 0.0f, mg = mw * cb;
-          in = fmaf(s == me ? 0.0f : mg, dl, in);
-          P[0][q][j] = fmaf(mw, dl, P[0][q][j]);
+          const float cb = keep ? G[0][q][j] : 0.0f, mw = m[o][j] * wt, with_delta = keep ? mw * (MAKES_C ? tab.delta[s] : delta) : 0.0f;
+          in = fmaf(s == me ? 0.0f : with_delta, cb, in);
+          P[0][q][j] += with_delta;
           if (!MAKES_C) {
             skip = s == me ? m[o][j] : skip;
-            all += mg;
-            gw[o][j] = cb * wt;
+            all = fmaf(keep ? mw : 0.0f, cb, all);
+            gw[o][j] = !SEQ || keep ? cb * wt : 0.0f;
           }
         }
       }
@@ -1190,6 +1219,75 @@ __device__ __forceinline__ double run_lanes(double v, int cut, int lane) {
   return v;
 }
 
+// Where a head's tokens hold what is not finite, the products of the main kernel may have met it times 0 at tokens that it is no
+// term of. Their elements that are not finite are summed again here without the masked terms, by a wave for each token:
+// dx of head h, and dB and dC of every rep-th token.
+template <int IO, bool SEQ>
+__device__ __forceinline__ void ssdb_mend(const SbArgs& a, int b, int c, int h) {
+  using T = typename Io<IO>::T;
+  const int lane = threadIdx.x & 63, n = a.d_state, rep = a.nheads / a.ngroups, grp = h / rep;
+  const int valid = min(kQ, a.seqlen - c * kQ);
+  const int64_t row0 = static_cast<int64_t>(b) * a.seqlen + static_cast<int64_t>(c) * kQ;
+  const int64_t bc = static_cast<int64_t>(b) * a.nchunks + c;
+  const T *const x = static_cast<const T*>(a.x) + row0 * a.x_row + lane, *const dy = static_cast<const T*>(a.dy) + row0 * a.dy_row + lane;
+  const T *const B = static_cast<const T*>(a.B) + row0 * a.b_row + grp * n, *const C = static_cast<const T*>(a.C) + row0 * a.c_row + grp * n;
+  auto wrong = [](float v) { return !(fabsf(v) < INFINITY); };
+  for (int t = threadIdx.x >> 6; t < valid; t += kQ / 64) {
+    const int first = SEQ ? max(a.begin[bc * kQ + t], 0) : 0, next = SEQ ? a.next[bc * kQ + t] : kQ, last = min(next, valid);
+    {
+      const int64_t bch = bc * a.nheads + h;
+      const double* cs = a.cs + bch * kQ;
+      T* const to = static_cast<T*>(a.dx) + ((row0 + t) * a.nheads + h) * kP + lane;
+      const bool mine = wrong(Io<IO>::load(to));
+      if (__any(mine)) {
+        float sum = 0.0f;
+        for (int r = t; r < last; ++r) {
+          float cb = 0.0f;
+          for (int k = lane; k < n; k += 64) cb = fmaf(Io<IO>::load(C + r * a.c_row + k), Io<IO>::load(B + t * a.b_row + k), cb);
+          sum = fmaf(decayed(cs[r] - cs[t]) * lanes_sum(cb, 64), Io<IO>::load(dy + r * a.dy_row + h * kP), sum);
+        }
+        if (next >= kQ) {
+          const float* R = a.R + (bch * kP + lane) * n;
+          float rb = 0.0f;
+          for (int k = 0; k < n; ++k) rb = fmaf(R[k], Io<IO>::load(B + t * a.b_row + k), rb);
+          sum = fmaf(decayed(cs[kQ - 1] - cs[t]), rb, sum);
+        }
+        if (mine) Io<IO>::store(to, fmaf(a.delta[bch * kQ + t], sum, a.D[h] * Io<IO>::load(dy + t * a.dy_row + h * kP)));
+      }
+    }
+    if (t % rep != h % rep) continue;
+    const int64_t row = ((row0 + t) * a.ngroups + grp) * n, whole = static_cast<int64_t>(a.batch) * a.seqlen * a.ngroups * n;
+    for (int of_c = 0; of_c < 2; ++of_c) {
+      T* const to = static_cast<T*>(of_c ? a.dC : a.dB) + row;
+      const float* const from = (of_c ? a.dCc : a.dBc) + row;
+      bool mine[2];
+      float sum[2] = {0.0f, 0.0f};
+      for (int i = 0; i < 2; ++i) {
+        const int k = lane + 64 * i;
+        mine[i] = k < n && wrong(Io<IO>::load(to + k));
+        if (mine[i])
+          for (int j = 0; j < a.csplit; ++j) sum[i] += from[j * whole + k];
+      }
+      if (!__any(mine[0] || mine[1])) continue;
+      for (int hh = grp * rep; hh < (grp + 1) * rep; ++hh) {
+        const int64_t bch = bc * a.nheads + hh;
+        const double* cs = a.cs + bch * kQ;
+        const float own = Io<IO>::load((of_c ? dy + t * a.dy_row : x + t * a.x_row) + hh * kP);
+        for (int o = of_c ? first : t; o < (of_c ? t + 1 : last); ++o) {
+          const float m = lanes_sum(own * Io<IO>::load((of_c ? x + o * a.x_row : dy + o * a.dy_row) + hh * kP), 64);
+          const float w = decayed(of_c ? cs[t] - cs[o] : cs[o] - cs[t]) * a.delta[bch * kQ + (of_c ? o : t)] * m;
+          for (int i = 0; i < 2; ++i) {
+            const int k = lane + 64 * i;
+            if (k < n) sum[i] = fmaf(w, Io<IO>::load((of_c ? B + o * a.b_row : C + o * a.c_row) + k), sum[i]);
+          }
+        }
+      }
+      for (int i = 0; i < 2; ++i)
+        if (mine[i]) Io<IO>::store(to + lane + 64 * i, sum[i]);
+    }
+  }
+}
+
 // 5. g and ddt of a chunk's tokens, and the chunk's sums for dA, ddt_bias and dD. A wave has a tile.
 template <int IO, bool SEQ>
 __global__ __launch_bounds__(kQ) void ssdb_step_kernel(const SbArgs a) {
@@ -1214,14 +1312,18 @@ __global__ __launch_bounds__(kQ) void ssdb_step_kernel(const SbArgs a) {
     for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
     if (lane == 0) pair[tile][tile - d] = s;
   }
-  const double s_m = tok(kOfS, m);
+  const float raw_s = tok(kOfS, m), raw_r = tok(kOfR, tid);
+  const double s_m = !SEQ || a.begin[bc * kQ + m] < 0 ? raw_s : 0.0f;
   down += run_lanes(late, 0, lane);
   const double from_s = run_lanes(s_m, 0, lane);
   if (lane == 63) of_s[tile] = from_s;
   down = __shfl(down + from_s, 63 - lane, 64);  // turned round
   // with tiles behind it, and from R: of the tokens before this one
-  const float delta = a.delta[bch * kQ + tid], of_r0 = tok(kOfR, tid);
-  const double col = tok(kColOut, tid), r = static_cast<double>(of_r0) * delta;
+  // (0 where nothing behind the tile, or behind the chunk, is of the token's document, whatever its delta)
+  const int next = SEQ ? a.next[bc * kQ + tid] : kQ;
+  const float delta = a.delta[bch * kQ + tid], of_r0 = !SEQ || next >= kQ ? raw_r : 0.0f;
+  const double col = !SEQ || next > (tid | (kTile - 1)) ? tok(kColOut, tid) : 0.0f;
+  const double r = !SEQ || next >= kQ ? static_cast<double>(of_r0) * delta : 0.0;
   const double up = run_lanes(col, 0, lane) - col, from_r = run_lanes(r, 0, lane);
   if (lane == 63) of_r[tile] = from_r;
   __syncthreads();
@@ -1261,6 +1363,8 @@ __global__ __launch_bounds__(kQ) void ssdb_step_kernel(const SbArgs a) {
     float* to = tid == 0 ? a.pA : tid == 1 ? a.pb : a.pD;
     to[bch] = (sums[tid][0] + sums[tid][1]) + (sums[tid][2] + sums[tid][3]);
   }
+  // a token's shares are not finite where its x, dy, B or C are not: infinity, or 0 times it, is in them
+  if (__syncthreads_or(!(fabsf(raw_s) < INFINITY && fabsf(raw_r) < INFINITY))) ssdb_mend<IO, SEQ>(a, b, c, h);
 }
 
 // dB and dC of the splits of the heads, one after the other.
@@ -1349,19 +1453,17 @@ hipError_t launch_typed(const SsdBwdCall& c, const SbArgs& a) {
   hipLaunchKernelGGL((ssdb_main_kernel<IO, N, SEQ>), dim3(static_cast<unsigned>((units + 7) / 8 * 8 * kTiles)), dim3(kMain), 0,
                      c.stream, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  hipLaunchKernelGGL((ssdb_step_kernel<IO, SEQ>), dim3(a.nchunks, a.nheads, a.batch), dim3(kQ), 0, c.stream, a);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  const int nblk = a.batch * a.nchunks;
-  if ((e = launch_part_sums(nblk, {{a.nheads, a.pA, a.dA}, {a.nheads, a.pb, a.ddt_bias}, {a.nheads, a.pD, a.dD}}, c.stream)) != hipSuccess)
-    return e;
   if (a.hsplit > 1) {
     using T = typename Io<IO>::T;
     const int64_t n4 = static_cast<int64_t>(a.batch) * a.seqlen * a.ngroups * N / 4;
     hipLaunchKernelGGL(ssdb_join_kernel<IO>, dim3(static_cast<unsigned>(std::min<int64_t>((n4 + 255) / 256, 65536)), 2), dim3(256),
                        0, c.stream, n4, a.hsplit, a.dBp, a.dCp, static_cast<T*>(a.dB), static_cast<T*>(a.dC));
-    return hipGetLastError();
+    if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  return hipSuccess;
+  hipLaunchKernelGGL((ssdb_step_kernel<IO, SEQ>), dim3(a.nchunks, a.nheads, a.batch), dim3(kQ), 0, c.stream, a);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  const int nblk = a.batch * a.nchunks;
+  return launch_part_sums(nblk, {{a.nheads, a.pA, a.dA}, {a.nheads, a.pb, a.ddt_bias}, {a.nheads, a.pD, a.dD}}, c.stream);
 }
 
 template <int IO, int N>
@@ -1382,6 +1484,7 @@ hipError_t launch_ssd_bwd(const SsdBwdCall& c) {
   a.seqlen = c.seqlen;
   a.nheads = c.nheads;
   a.ngroups = c.ngroups;
+  a.d_state = c.d_state;
   a.nchunks = (c.seqlen + kQ - 1) / kQ;
   a.hsplit = heads_split(c.batch, a.nchunks, c.nheads, c.ngroups, kTiles, 4);
   a.per = (c.nheads / c.ngroups + a.hsplit - 1) / a.hsplit;

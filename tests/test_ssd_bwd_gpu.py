@@ -250,3 +250,67 @@ def test_two_calls_at_once():
         torch.cuda.synchronize()
         for i in range(2):
             assert all(torch.equal(got[i][n], want[i][n]) for n in want[i])
+
+
+@pytest.mark.parametrize("what", ["all nan", "all inf", "one x", "one B", "one dy", "one C", "dt"])
+@pytest.mark.parametrize("N,G,dtype", [(64, 2, "f32"), (128, 1, "f32"), (64, 1, "bf16"), (128, 1, "bf16")])
+def test_what_is_not_finite_stays_in_its_document(N, G, dtype, what):
+    """Documents begin inside tiles, at a tile's and behind a chunk's edge; what the second and the fifth hold is not
+    finite. The others' gradients are those of finite inputs, to the same bounds."""
+    b, L, H = 2, 700, 4
+    a = make(b, L, H, G, N, dtype, seed=11, state=True)
+    ids = torch.zeros(b, L, dtype=torch.int32)
+    for n, at in enumerate((37, 101, 192, 300, 517, 640)):
+        ids[:, at:] = n + 1
+    a["seq_idx"] = ids
+    bad = (ids == 1) | (ids == 4)
+    bad[0] = ids[0] == 1
+    clean = ~bad.numpy()
+    want, tol = oracle_ssd_bwd(**a), bounds(a)
+    g = {n: t.clone() if isinstance(t, torch.Tensor) else t for n, t in a.items()}
+    value = float("nan") if what == "all nan" else float("inf")
+    for n in ("x", "dt", "B", "C", "dy"):
+        if what.startswith("all"):
+            g[n][bad] = value
+        elif what == "dt" == n:
+            g[n][bad] = float("nan")
+        elif what == "one " + n:
+            g[n][0, 60, 0, 5] = value
+            g[n][1, 400, -1, -1] = -value
+    say(what, N, G, dtype)
+    got = call(gpu(g))
+    torch.cuda.synchronize()
+    for n in ("dx", "ddt", "dB", "dC"):
+        rounded = dtype == "bf16"
+        t = tol[n] + (BF * (np.abs(want[n]) + tol[n]) if rounded else 0) + 1e-37
+        v = f64(got[n])
+        assert np.isfinite(v[clean]).all(), n
+        assert (np.abs(v - want[n]) <= t)[clean].all(), n
+        if what.startswith("all"):
+            assert not np.isfinite(v[~clean]).any(), n
+    assert (np.abs(f64(got["dstate"]) - want["dstate"]) <= tol["dstate"] + 1e-37).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_what_is_not_finite_reaches_what_it_is_a_term_of(dtype):
+    """Without documents: x and B of a token are terms of its own dx and dB and of dC from it on, C and dy of its own dC
+    and of dx and dB up to it."""
+    a = make(1, 330, 2, 1, 128, dtype, seed=12, state=True)
+    want, tol = oracle_ssd_bwd(**a), bounds(a)
+    for names, at in ((("x", "B"), 40), (("C", "dy"), 290), (("C", "dy"), 20)):
+        g = {n: t.clone() if isinstance(t, torch.Tensor) else t for n, t in a.items()}
+        for n in names:
+            g[n][0, at] = float("nan")
+        say(names, at, dtype)
+        got = call(gpu(g))
+        torch.cuda.synchronize()
+        t = np.arange(330)
+        for n in ("dx", "dB", "dC"):
+            if names[0] == "x":
+                free = t < at if n == "dC" else t != at
+            else:
+                free = t != at if n == "dC" else t > at
+            bound = tol[n] + (BF * (np.abs(want[n]) + tol[n]) if dtype == "bf16" else 0) + 1e-37
+            v = f64(got[n])
+            assert (np.abs(v - want[n]) <= bound)[0, free].all(), n
+            assert not np.isfinite(v[0, at]).any(), n
