@@ -285,10 +285,10 @@ struct SbArgs {
   float *dBc, *dCc;    // [csplit][batch][seqlen][ngroups][N]: what the states carry
   float *pA, *pb, *pD; // [batch][chunk][heads]
 };
-// What the step kernel has of each token: its row of m inside its tile (before the token) and over the three tiles before
+// What the step kernel has of each token: its row of m inside its tile (before the token; in two floats, as its column) and over the three tiles before
 // it, nearest first; its column inside its tile and over the tiles behind it; its shares in g of S and, without delta, of
 // R, whether or not these reach it; x . dx without delta and D, but for R's share; dy . x.
-enum { kRowIn, kRow1, kRow2, kRow3, kColIn, kColOut, kOfS, kOfR, kDirect, kSkip, kTokSums };
+enum { kRowIn, kRow1, kRow2, kRow3, kColIn, kColOut, kOfS, kOfR, kDirect, kSkip, kRowInLess, kColInLess, kTokSums };
 
 // exp of a difference of running sums, at most 0
 __device__ __forceinline__ float decayed(double d) { return exp2_hw(fminf(static_cast<float>(d) * kLog2e, 0.0f)); }
@@ -486,6 +486,16 @@ __device__ __forceinline__ float over_g(float v) {
   u = __float_as_uint(__uint_as_float(r[0]) + __uint_as_float(r[1]));
   r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ double over_g(double v) {
+#pragma unroll
+  for (int step = 0; step < 2; ++step) {
+    const uint32_t lo = static_cast<uint32_t>(__double2loint(v)), hi = static_cast<uint32_t>(__double2hiint(v));
+    const auto l = step == 0 ? __builtin_amdgcn_permlane16_swap(lo, lo, false, false) : __builtin_amdgcn_permlane32_swap(lo, lo, false, false);
+    const auto u = step == 0 ? __builtin_amdgcn_permlane16_swap(hi, hi, false, false) : __builtin_amdgcn_permlane32_swap(hi, hi, false, false);
+    v = __hiloint2double(static_cast<int>(u[0]), static_cast<int>(l[0])) + __hiloint2double(static_cast<int>(u[1]), static_cast<int>(l[1]));
+  }
+  return v;
 }
 
 // 3. What the states are of dC (from S and dy) or of dB (from R and x), a chunk's 256 tokens at a time, with each token's
@@ -940,7 +950,8 @@ __device__ __forceinline__ void ssdb_task(const SbArgs& a, const MainPlace& pl, 
     };
     // the own tile: a place of m has the same bits in its row and in its column, of which the step kernel takes one from
     // the other
-    float in = 0.0f, all = 0.0f, skip = 0.0f;
+    double in = 0.0;
+    float all = 0.0f, skip = 0.0f;
     auto inside = [&](int half) {
       f4 m[2], gw[2];
       scores(MAKES_C ? xi : yi, half, mine, m);
@@ -953,7 +964,7 @@ __device__ __forceinline__ void ssdb_task(const SbArgs& a, const MainPlace& pl, 
           const float wt = decayed(MAKES_C ? cs_me - tab.cs[s] : tab.cs[s] - cs_me);
           const bool keep = MAKES_C ? s <= me && (!SEQ || s >= begin) : s >= me && (!SEQ || s < next);
           const float cb = keep ? G[0][q][j] : 0.0f, mw = m[o][j] * wt, with_delta = keep ? mw * (MAKES_C ? tab.delta[s] : delta) : 0.0f;
-          in = fmaf(s == me ? 0.0f : with_delta, cb, in);
+          in += s == me ? 0.0f : with_delta * cb;
           P[0][q][j] += with_delta;
           if (!MAKES_C) {
             skip = s == me ? m[o][j] : skip;
@@ -969,6 +980,11 @@ __device__ __forceinline__ void ssdb_task(const SbArgs& a, const MainPlace& pl, 
         for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(in), "+v"(all), "+v"(P[0][q][j]));
     };
     float* const tok = a.tok + bch * kQ + me;
+    auto put_two = [&](float* to, int more, int less, double v) {
+      const float m = static_cast<float>(v);
+      to[more * a.tok_step] = m;
+      to[less * a.tok_step] = static_cast<float>(v - m);
+    };
 
     if constexpr (MAKES_C) {
       // what comes from the gradient behind the chunk, for the other task
@@ -1035,7 +1051,7 @@ __device__ __forceinline__ void ssdb_task(const SbArgs& a, const MainPlace& pl, 
       }
       renew(l, gg);
       in = over_g(in);
-      if (gg == 0) tok[kRowIn * a.tok_step] = in;
+      if (gg == 0) put_two(tok, kRowIn, kRowInLess, in);
 #pragma unroll
       for (int d = 1; d <= FAR; ++d) {
         out[d] = over_g(out[d]);
@@ -1085,7 +1101,7 @@ __device__ __forceinline__ void ssdb_task(const SbArgs& a, const MainPlace& pl, 
         }
       }
       if (gg == 0) {
-        tok[kColIn * a.tok_step] = in;
+        put_two(tok, kColIn, kColInLess, in);
         tok[kColOut * a.tok_step] = delta * column;
         tok[kDirect * a.tok_step] = all + column;
         tok[kSkip * a.tok_step] = skip;
@@ -1300,9 +1316,10 @@ __global__ __launch_bounds__(kQ) void ssdb_step_kernel(const SbArgs a) {
   const int64_t row = static_cast<int64_t>(b) * a.seqlen + static_cast<int64_t>(c) * kQ + tid;
   const int m = tile * kTile + kTile - 1 - lane;  // from the tile's last token on
   auto tok = [&](int n, int t) { return t < valid ? a.tok[n * a.tok_step + bch * kQ + t] : 0.0f; };
+  auto two = [&](int more, int less) { return static_cast<double>(tok(more, m)) + tok(less, m); };
   // inside the tile
   const bool cut_m = SEQ && lane > 0 && a.next[bc * kQ + m] == m + 1;
-  double down = run_lanes(static_cast<double>(tok(kRowIn, m)) - tok(kColIn, m), cut_m, lane);
+  double down = run_lanes(two(kRowIn, kRowInLess) - two(kColIn, kColInLess), cut_m, lane);
   // from tiles before it, and from S
   double late = 0.0;
   for (int d = 1; d <= tile; ++d) {
