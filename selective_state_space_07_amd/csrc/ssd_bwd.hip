@@ -1309,7 +1309,7 @@ template <int IO, bool SEQ>
 __global__ __launch_bounds__(kQ) void ssdb_step_kernel(const SbArgs a) {
   using T = typename Io<IO>::T;
   __shared__ double of_s[kTiles], of_r[kTiles], pair[kTiles][kTiles];  // sums of tiles, and of m over two tiles
-  __shared__ float sums[3][kTiles];
+  __shared__ double sums[3][kTiles];
   const int tid = threadIdx.x, lane = tid & 63, tile = tid >> 6, c = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   const int valid = min(kQ, a.seqlen - c * kQ);
   const int64_t bc = static_cast<int64_t>(b) * a.nchunks + c, bch = bc * a.nheads + h;
@@ -1358,27 +1358,24 @@ __global__ __launch_bounds__(kQ) void ssdb_step_kernel(const SbArgs a) {
     g += whole * decay;
   }
   if (SEQ && a.begin[bc * kQ + tid] == tid) g = 0.0;  // nothing reaches a document's first token
-  float dA = 0.0f, db = 0.0f, dD = 0.0f;
+  double all[3] = {};  // of dA, ddt_bias and dD: terms of either sign, many of which cancel
   if (tid < valid) {
     const float v = Io<IO>::load(static_cast<const T*>(a.dt) + row * a.dt_row + h) + a.dt_bias[h];
-    const float d = fmaf(a.A[h], static_cast<float>(g), tok(kDirect, tid) + of_r0) * sigmoid(v).s;
-    Io<IO>::store(static_cast<T*>(a.ddt) + row * a.nheads + h, d);
-    dA = static_cast<float>(g) * delta;
-    db = d;
-    dD = tok(kSkip, tid);
+    const double d = (static_cast<double>(a.A[h]) * g + (static_cast<double>(tok(kDirect, tid)) + of_r0)) * (1.0f / (1.0f + expf(-v)));
+    Io<IO>::store(static_cast<T*>(a.ddt) + row * a.nheads + h, static_cast<float>(d));
+    all[0] = g * delta;
+    all[1] = d;
+    all[2] = tok(kSkip, tid);
   }
-  dA = lanes_sum(dA, 64);
-  db = lanes_sum(db, 64);
-  dD = lanes_sum(dD, 64);
-  if (lane == 0) {
-    sums[0][tile] = dA;
-    sums[1][tile] = db;
-    sums[2][tile] = dD;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    for (int o = 32; o > 0; o >>= 1) all[i] += __shfl_xor(all[i], o, 64);
+    if (lane == 0) sums[i][tile] = all[i];
   }
   __syncthreads();
   if (tid < 3) {
     float* to = tid == 0 ? a.pA : tid == 1 ? a.pb : a.pD;
-    to[bch] = (sums[tid][0] + sums[tid][1]) + (sums[tid][2] + sums[tid][3]);
+    to[bch] = static_cast<float>((sums[tid][0] + sums[tid][1]) + (sums[tid][2] + sums[tid][3]));
   }
   // a token's shares are not finite where its x, dy, B or C are not: infinity, or 0 times it, is in them
   if (__syncthreads_or(!(fabsf(raw_s) < INFINITY && fabsf(raw_r) < INFINITY))) ssdb_mend<IO, SEQ>(a, b, c, h);
