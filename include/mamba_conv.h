@@ -35,8 +35,8 @@
  *   bias             [channels] float32, or NULL (zeros)
  *   seq_idx          [batch][seqlen] int32, or NULL (one document per row)
  *   states           [batch][channels][taps - 1] float32
- * Element alignment is enough (16-byte alignment of pointers, rows and parts
- * runs faster). channels <= 2^20; batch <= 2^24; batch * seqlen < 2^31. Inputs
+ * Element alignment is enough (pointers, rows and parts at multiples of four
+ * elements run faster). channels <= 2^20; batch <= 2^24; batch * seqlen < 2^30. Inputs
  * may overlap one another, outputs nothing.
  */
 #ifndef MAMBA_CONV_H

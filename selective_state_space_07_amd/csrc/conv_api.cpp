@@ -20,7 +20,8 @@ int check_dims(int32_t batch, int32_t seqlen, int32_t channels, int32_t taps, in
   if (taps < 2 || taps > 4) return fail(MAMBA_ERR_SHAPE, "taps must be 2, 3 or 4 (got %d)", taps);
   if (channels > (1 << 20) || batch > (1 << 24))
     return fail(MAMBA_ERR_SHAPE, "channels must be <= 2^20 and batch <= 2^24 (got %d, %d)", channels, batch);
-  if (!below_2_31({batch, seqlen})) return fail(MAMBA_ERR_SHAPE, "batch * seqlen must be below 2^31");
+  // (a run's end, and the tokens fetched ahead of it, are int32 numbers)
+  if (!below_2_31({2, batch, seqlen})) return fail(MAMBA_ERR_SHAPE, "batch * seqlen must be below 2^30");
   if (io_dtype != MAMBA_F32 && io_dtype != MAMBA_BF16)
     return fail(MAMBA_ERR_DTYPE, "io_dtype must be MAMBA_F32 (0) or MAMBA_BF16 (1), got %d", io_dtype);
   return MAMBA_OK;

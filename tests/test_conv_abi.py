@@ -110,3 +110,12 @@ def test_front_end_refusals():
     for split in ((4, 5), (8, 0), (1, 1, 1, 1, 4), ()):
         with pytest.raises(_b.MambaScanError):
             conv._sizes(split, 8)
+
+
+def test_as_many_tokens_as_numbers_hold(lib):
+    """A run's end and the tokens read ahead of it are int32 numbers."""
+    for what in ("fwd", "bwd"):
+        assert call(lib, what, b=1, L=1 << 30) == 2 and "2^30" in ms.mamba_scan_last_error()
+        assert call(lib, what, b=1, L=(1 << 30) - 1, ids=0) != 2 or "2^30" not in ms.mamba_scan_last_error()
+    assert ms.conv_workspace_bytes(1, 1 << 30, 8, 4, torch.float32) == 0
+    assert ms.conv_workspace_bytes(1, (1 << 30) - 1, 8, 4, torch.float32) > 0
