@@ -92,7 +92,7 @@ int mamba2_ssd_step(int32_t batch, int32_t nheads, int32_t headdim, int32_t d_st
 
 /* Bytes of device workspace mamba2_ssd_bwd needs (0 for shapes it rejects): a
    float32 state and its gradient per (batch row, chunk of 256 steps, head), and
-   some 12 KB more; dB and dC in float32, several times where a group's heads are
+   some 16 KB more; dB and dC in float32, several times where a group's heads are
    split over workgroups. */
 size_t mamba2_ssd_bwd_workspace_bytes(int32_t batch, int32_t seqlen, int32_t nheads, int32_t headdim, int32_t d_state,
                                       int32_t ngroups, int32_t io_dtype);

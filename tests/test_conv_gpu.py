@@ -302,3 +302,43 @@ def test_past_two_to_the_31_elements():
     tail = ms.conv_bwd(x[:, L - n:], w, y2, bias, before)
     torch.cuda.synchronize()
     assert torch.equal(grads["dx"][:, L - n:], tail["dx"])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("act", ["silu", "none"])
+@pytest.mark.parametrize("docs", [0, 7])
+@pytest.mark.parametrize("k", [2, 3, 4])
+@pytest.mark.parametrize("c", [260, 67])
+def test_every_kernel(c, k, docs, act, dtype):
+    """Taps, documents, activations, types, and channels by four and one by one: a kernel for each."""
+    for L in (1, 2, 3, 5, 38, 1027):
+        a, dy, ds = make(2, L, c, k, DT[dtype], seed=L + k, state=True, docs=docs)
+        g = cuda(a)
+        print(c, k, docs, act, dtype, L, flush=True)
+        got = ms.conv_fwd(**g, activation=act)
+        grads = ms.conv_bwd(dy=dy.cuda(), dstate=cuda(ds), activation=act, **g)
+        torch.cuda.synchronize()
+        check_fwd(a, got, act, "every")
+        check_bwd(a, dy, ds, grads, act, "every")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_another_documents_values_reach_none(value, dtype):
+    """x and dy of the second document, which begins and ends inside runs, hold nothing finite."""
+    a, dy, ds = make(2, 150, 72, 4, DT[dtype], seed=5, state=True)
+    ids = torch.zeros(2, 150, dtype=torch.int32)
+    ids[:, 21:] = 1
+    ids[:, 90:] = 2
+    a["seq_idx"] = ids
+    clean = (ids != 1).numpy()
+    y0, s0 = ms.conv_fwd(**cuda(a))
+    d0 = ms.conv_bwd(dy=dy.cuda(), dstate=cuda(ds), **cuda(a))
+    a["x"][:, 21:90] = value
+    dy[:, 21:90] = value
+    y1, s1 = ms.conv_fwd(**cuda(a))
+    d1 = ms.conv_bwd(dy=dy.cuda(), dstate=cuda(ds), **cuda(a))
+    torch.cuda.synchronize()
+    for u, v in ((y0, y1), (d0["dx"], d1["dx"])):
+        assert torch.equal(u.cpu()[clean], v.cpu()[clean])
+    assert torch.equal(s0, s1) and torch.equal(d0["dstate"], d1["dstate"])
