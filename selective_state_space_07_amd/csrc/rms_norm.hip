@@ -407,6 +407,8 @@ hipError_t launch_typed(const RnCall& c, const Layout& l, const RnArgs& a) {
       hipLaunchKernelGGL((rms_fwd_kernel<IO, R, V, K, WIDE, 1>), grid, block, 0, c.stream, a);
     else
       hipLaunchKernelGGL((rms_fwd_kernel<IO, R, V, K, WIDE, 2>), grid, block, 0, c.stream, a);
+  } else {
+    return hipErrorInvalidValue;  // 8-bit outputs are written by pieces alone
   }
   return hipGetLastError();
 }
@@ -433,11 +435,12 @@ size_t rn_part_floats(int64_t rows, int32_t channels, int32_t io_dtype) {
 }
 
 hipError_t launch_rmsnorm(const RnCall& c) {
-  const int full = c.io_dtype == 0 ? 4 : 8;
-  auto fits = [&](const void* p, int64_t row) { return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && row % full == 0); };
-  const bool can_vec = fits(c.x, c.x_row) && fits(c.residual, c.residual_row) && fits(c.h, c.h_row) &&
-                       fits(c.dy, c.dy_row) && fits(c.dh, c.dh_row) && fits(c.y, 0) && fits(c.h_out, 0) && fits(c.dx, 0) &&
-                       fits(c.dresidual, 0);
+  // 16 bytes of each tensor's own type: a piece of eight bfloat16 channels meets a float32 residual as two of four
+  const int64_t es = c.io_dtype == 0 ? 4 : 2, rs = c.residual_dtype == 0 ? 4 : 2;
+  auto fits = [](const void* p, int64_t row_bytes) { return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && row_bytes % 16 == 0); };
+  const bool can_vec = fits(c.x, c.x_row * es) && fits(c.residual, c.residual_row * rs) && fits(c.h, c.h_row * rs) &&
+                       fits(c.dy, c.dy_row * es) && fits(c.dh, c.dh_row * rs) && fits(c.y, 0) && fits(c.h_out, 0) &&
+                       fits(c.dx, 0) && fits(c.dresidual, 0);
   const Layout l = layout(c.channels, c.io_dtype, can_vec);
   RnArgs a{};
   a.rows = c.rows;
