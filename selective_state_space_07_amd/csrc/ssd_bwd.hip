@@ -288,7 +288,7 @@ struct SbArgs {
   float *ddt_bias, *dA, *dD, *dstate_in;
   // workspace; "bch" numbers (batch row, chunk, head)
   float *S, *R;        // [bch][64][N]
-  float* decay;        // [bch]: over the chunk, 0 where a document begins in it
+  float* decay;        // [bch]: over the chunk, -1 where a document begins in it
   double* cs;          // [bch][256]
   float* delta;        // [bch][256]
   int32_t *begin, *next;  // [batch][chunk][256]: the latest document begin up to a token (-1: none), the first behind it (256)
@@ -404,7 +404,7 @@ __global__ __launch_bounds__(kState) void ssdb_state_kernel(const SbArgs a) {
     a.cs[bch * kQ + tid] = cs;
     a.delta[bch * kQ + tid] = delta;
     // (a begin at the first token leaves ends[0] at 0 as well, and ends[1] too)
-    if (tid == 0) a.decay[bch] = open ? decayed(cs_end) : 0.0f;
+    if (tid == 0) a.decay[bch] = open ? decayed(cs_end) : -1.0f;
   }
   w[tid] = tid < first || tid >= last ? 0.0f : which == 0 ? decayed(cs_end - cs) * delta : decayed(cs);
   const T* X = (which == 0 ? static_cast<const T*>(a.x) + row0 * a.x_row : static_cast<const T*>(a.dy) + row0 * a.dy_row) + h * kP;
@@ -486,8 +486,8 @@ __global__ __launch_bounds__(kState) void ssdb_pass_kernel(const SbArgs a, int n
       if (i0 + i >= n) break;
       all[slot(i0 + i) * n4 + e] = s;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)  // past a document's begin nothing is carried, whatever it was
-        s[j] = d[i] == 0.0f ? own[i][j] : fmaf(d[i], s[j], own[i][j]);
+      for (int j = 0; j < 4; ++j)  // past a document's begin nothing is carried, whatever it was; past a decay of 0 what is not finite
+        s[j] = d[i] < 0.0f ? own[i][j] : fmaf(d[i], s[j], own[i][j]);
     }
   }
   if (which == 1 && a.dstate_in) reinterpret_cast<f4*>(a.dstate_in)[bh * n4 + e] = s;
@@ -1366,7 +1366,7 @@ __global__ __launch_bounds__(kQ) void ssdb_step_kernel(const SbArgs a) {
       for (int k = 0; k < tile; ++k) g += pair[j][k];
   }
   const float decay = a.decay[bch];
-  if (decay != 0.0f) {
+  if (!(decay < 0.0f)) {
     double whole = 0.0;
     for (int i = 0; i < 16; ++i) whole += a.dot[bch * 16 + i];
     g += whole * decay;
