@@ -304,6 +304,9 @@ struct SbArgs {
 // R, whether or not these reach it; x . dx without delta and D, but for R's share; dy . x.
 enum { kRowIn, kRow1, kRow2, kRow3, kColIn, kColOut, kOfS, kOfR, kDirect, kSkip, kRowInLess, kColInLess, kTokSums };
 
+// Steps of the exponent. Nothing is left of float32 behind one of kGone or less (2^-150 and less); one below kLeast, -infinity
+// among them, counts as kLeast: it leaves as little, and the sums behind it keep the bits that their differences need.
+constexpr double kGone = -104.0, kLeast = -512.0;
 // exp of a difference of running sums, at most 0
 __device__ __forceinline__ float decayed(double d) { return exp2_hw(fminf(static_cast<float>(d) * kLog2e, 0.0f)); }
 
@@ -371,7 +374,8 @@ __global__ __launch_bounds__(kState) void ssdb_state_kernel(const SbArgs a) {
   // the running sum; a document's begin starts it again, so that what another holds is no part of it
   bool restart = false;
   if (SEQ) restart = tid < valid && static_cast<int64_t>(c) * kQ + tid > 0 && a.seq_idx[row0 + tid] != a.seq_idx[row0 + tid - 1];
-  double own = static_cast<double>(delta) * a.A[h];
+  double own = tid < valid ? static_cast<double>(delta) * a.A[h] : 0.0;
+  own = own < kLeast ? kLeast : own;
   asm volatile("" : "+v"(own));  // rounded here, and not with the first sum
   const double cs = SEQ ? scan256_runs(own, restart, part, ipart, tid) : scan256(own, part, tid, [](double p, double q) { return p + q; });
   if (SEQ) __syncthreads();
@@ -1331,9 +1335,13 @@ __global__ __launch_bounds__(kQ) void ssdb_step_kernel(const SbArgs a) {
   const int m = tile * kTile + kTile - 1 - lane;  // from the tile's last token on
   auto tok = [&](int n, int t) { return t < valid ? a.tok[n * a.tok_step + bch * kQ + t] : 0.0f; };
   auto two = [&](int more, int less) { return static_cast<double>(tok(more, m)) + tok(less, m); };
-  // inside the tile
-  const bool cut_m = SEQ && lane > 0 && a.next[bc * kQ + m] == m + 1;
-  double down = run_lanes(two(kRowIn, kRowInLess) - two(kColIn, kColInLess), cut_m, lane);
+  const float delta = a.delta[bch * kQ + tid];
+  const bool gone = static_cast<double>(delta) * a.A[h] <= kGone;  // at this token, whose g is 0 times what it would be
+  const bool gone_m = __shfl(static_cast<int>(gone), 63 - lane), gone_next = __shfl(static_cast<int>(gone), (64 - lane) & 63);
+  // inside the tile; no term reaches over a document's begin, or over a step of which nothing is left
+  const bool cut_m = lane > 0 && (gone_next || (SEQ && a.next[bc * kQ + m] == m + 1));
+  const double row_m = two(kRowIn, kRowInLess);
+  double down = run_lanes(row_m - two(kColIn, kColInLess), cut_m, lane);
   // from tiles before it, and from S
   double late = 0.0;
   for (int d = 1; d <= tile; ++d) {
@@ -1348,17 +1356,19 @@ __global__ __launch_bounds__(kQ) void ssdb_step_kernel(const SbArgs a) {
   down += run_lanes(late, 0, lane);
   const double from_s = run_lanes(s_m, 0, lane);
   if (lane == 63) of_s[tile] = from_s;
-  down = __shfl(down + from_s, 63 - lane, 64);  // turned round
+  // (the token's own row is 0 times what is before it)
+  down = __shfl(gone_m ? row_m + late + s_m : down + from_s, 63 - lane, 64);  // turned round
   // with tiles behind it, and from R: of the tokens before this one
   // (0 where nothing behind the tile, or behind the chunk, is of the token's document, whatever its delta)
   const int next = SEQ ? a.next[bc * kQ + tid] : kQ;
-  const float delta = a.delta[bch * kQ + tid], of_r0 = !SEQ || next >= kQ ? raw_r : 0.0f;
+  const float of_r0 = !SEQ || next >= kQ ? raw_r : 0.0f;
   const double col = !SEQ || next > (tid | (kTile - 1)) ? tok(kColOut, tid) : 0.0f;
   const double r = !SEQ || next >= kQ ? static_cast<double>(of_r0) * delta : 0.0;
-  const double up = run_lanes(col, 0, lane) - col, from_r = run_lanes(r, 0, lane);
+  const double upto = run_lanes(col + r, 0, lane), before = __shfl_up(upto, 1, 64);
+  const double from_r = run_lanes(r, 0, lane);
   if (lane == 63) of_r[tile] = from_r;
   __syncthreads();
-  double g = down + up + (from_r - r);
+  double g = lane > 0 ? down + before : down;
   for (int j = 0; j < kTiles; ++j) {
     if (j > tile) g += of_s[j];
     if (j < tile) g += of_r[j];
@@ -1371,6 +1381,7 @@ __global__ __launch_bounds__(kQ) void ssdb_step_kernel(const SbArgs a) {
     for (int i = 0; i < 16; ++i) whole += a.dot[bch * 16 + i];
     g += whole * decay;
   }
+  if (gone) g = down;
   if (SEQ && a.begin[bc * kQ + tid] == tid) g = 0.0;  // nothing reaches a document's first token
   double all[3] = {};  // of dA, ddt_bias and dD: terms of either sign, many of which cancel
   if (tid < valid) {
