@@ -119,8 +119,11 @@ size_t mamba2_ssd_bwd_workspace_bytes(int32_t batch, int32_t seqlen, int32_t nhe
  *
  * What is not finite reaches, of dx, ddt, dB, dC and dstate_in, only what it is
  * a term of: no other document's with seq_idx, and of dx, dB and dC no token
- * that does not meet it. What it does reach may be NaN where it is infinite. A
- * head and chunk that holds it takes longer.
+ * that does not meet it. What it does reach is not finite, and may be NaN where
+ * it is infinite. A head and chunk that holds it takes longer. A dt that is NaN
+ * is so met by dx and dB up to its token and by dC from it on; so is an infinite
+ * one, but that the tokens before it do not meet it (its decay is 0). Where the
+ * product delta A is NaN, delta counts as NaN.
  */
 int mamba2_ssd_bwd(int32_t batch, int32_t seqlen, int32_t nheads, int32_t headdim, int32_t d_state, int32_t ngroups,
                    int32_t io_dtype, const void* x, int64_t x_stride, const void* dt, int64_t dt_stride, const void* B,

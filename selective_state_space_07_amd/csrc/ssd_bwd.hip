@@ -290,7 +290,7 @@ struct SbArgs {
   float *S, *R;        // [bch][64][N]
   float* decay;        // [bch]: over the chunk, -1 where a document begins in it
   double* cs;          // [bch][256]
-  float* delta;        // [bch][256]
+  float* delta;        // [bch][256]; its sign is set where a step behind the token, of its document and chunk, is NaN
   int32_t *begin, *next;  // [batch][chunk][256]: the latest document begin up to a token (-1: none), the first behind it (256)
   float* dot;          // [bch][16]: shares of <R, S>
   float* tok;          // [kTokSums][bch][256]
@@ -306,7 +306,10 @@ enum { kRowIn, kRow1, kRow2, kRow3, kColIn, kColOut, kOfS, kOfR, kDirect, kSkip,
 
 // Steps of the exponent. Nothing is left of float32 behind one of kGone or less (2^-150 and less); one below kLeast, -infinity
 // among them, counts as kLeast: it leaves as little, and the sums behind it keep the bits that their differences need.
+// One that is NaN counts as kLeast too, so that the differences behind it are numbers; its delta is NaN, which is in all that
+// the tokens from it on have of it, and the tokens before it, which meet its decay, have NaN for a delta of their own.
 constexpr double kGone = -104.0, kLeast = -512.0;
+__device__ __forceinline__ float own_delta(float d) { return __float_as_int(d) < 0 ? __builtin_nanf("") : d; }
 // exp of a difference of running sums, at most 0
 __device__ __forceinline__ float decayed(double d) { return exp2_hw(fminf(static_cast<float>(d) * kLog2e, 0.0f)); }
 
@@ -362,6 +365,7 @@ __global__ __launch_bounds__(kState) void ssdb_state_kernel(const SbArgs a) {
   __shared__ __attribute__((aligned(16))) float w[kQ];
   __shared__ double part[4], cs_end;
   __shared__ int ipart[4], ends[2];
+  __shared__ uint8_t marks[kQ];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, l15 = lane & 15, g = lane >> 4;
   const int which = blockIdx.x & 1, c = blockIdx.x >> 1, h = blockIdx.y, b = blockIdx.z;
   const int grp = h / (a.nheads / a.ngroups);
@@ -375,7 +379,9 @@ __global__ __launch_bounds__(kState) void ssdb_state_kernel(const SbArgs a) {
   bool restart = false;
   if (SEQ) restart = tid < valid && static_cast<int64_t>(c) * kQ + tid > 0 && a.seq_idx[row0 + tid] != a.seq_idx[row0 + tid - 1];
   double own = tid < valid ? static_cast<double>(delta) * a.A[h] : 0.0;
-  own = own < kLeast ? kLeast : own;
+  const bool lost = !(own < INFINITY);
+  if (lost) delta = __builtin_nanf("");
+  own = lost || own < kLeast ? kLeast : own;
   asm volatile("" : "+v"(own));  // rounded here, and not with the first sum
   const double cs = SEQ ? scan256_runs(own, restart, part, ipart, tid) : scan256(own, part, tid, [](double p, double q) { return p + q; });
   if (SEQ) __syncthreads();
@@ -398,7 +404,14 @@ __global__ __launch_bounds__(kState) void ssdb_state_kernel(const SbArgs a) {
       if (tid == 0) a.next[bc * kQ + kQ - 1] = kQ;
     }
   }
-  __syncthreads();
+  bool tainted = false, behind = false;  // a step behind the token, of its document, is NaN; one up to it, from the chunk's first on
+  const bool any_lost = __syncthreads_or(lost);
+  if (any_lost) {
+    marks[tid] = static_cast<uint8_t>(lost | restart << 1);
+    __syncthreads();
+    for (int t = tid + 1; t < valid && !(marks[t] & 2); ++t) tainted |= marks[t] & 1;
+    for (int t = 0; t <= tid; ++t) behind |= marks[t] & 1;
+  }
   const bool open = !SEQ || (ends[1] == valid && ends[0] == 0);  // no document begins behind the chunk's first token
   if (SEQ) {
     if (which == 0) first = ends[0];
@@ -406,11 +419,11 @@ __global__ __launch_bounds__(kState) void ssdb_state_kernel(const SbArgs a) {
   }
   if (which == 0) {
     a.cs[bch * kQ + tid] = cs;
-    a.delta[bch * kQ + tid] = delta;
+    a.delta[bch * kQ + tid] = __builtin_copysignf(delta, tainted ? -1.0f : 1.0f);
     // (a begin at the first token leaves ends[0] at 0 as well, and ends[1] too)
-    if (tid == 0) a.decay[bch] = open ? decayed(cs_end) : -1.0f;
+    if (tid == 0) a.decay[bch] = !open ? -1.0f : any_lost ? __builtin_nanf("") : decayed(cs_end);
   }
-  w[tid] = tid < first || tid >= last ? 0.0f : which == 0 ? decayed(cs_end - cs) * delta : decayed(cs);
+  w[tid] = tid < first || tid >= last ? 0.0f : which == 0 ? decayed(cs_end - cs) * delta : behind ? __builtin_nanf("") : decayed(cs);
   const T* X = (which == 0 ? static_cast<const T*>(a.x) + row0 * a.x_row : static_cast<const T*>(a.dy) + row0 * a.dy_row) + h * kP;
   const T* Bc = (which == 0 ? static_cast<const T*>(a.B) + row0 * a.b_row : static_cast<const T*>(a.C) + row0 * a.c_row) + grp * N;
   const int64_t ldx = which == 0 ? a.x_row : a.dy_row, ldb = which == 0 ? a.b_row : a.c_row;
@@ -613,7 +626,7 @@ __device__ __forceinline__ void ssdb_carry(const SbArgs& a, int u, char* lds) {
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) now[k][kb] = f[k][kb];
       e[k] = decayed(OF_C ? cs[k] : end - cs[k]);
-      de[k] = OF_C ? e[k] : delta[k] * e[k];
+      de[k] = OF_C ? e[k] : own_delta(delta[k]) * e[k];
     }
     __syncthreads();
     fetch(h + 1 < h1 ? h + 1 : h);
@@ -775,7 +788,7 @@ struct MainFill {
       MainTables& tab = reinterpret_cast<MainTables*>(lds + M::kTab)[buf];
       tab.cs[tid] = cs;
       tab.delta[tid] = delta;
-      tab.to_end[tid] = decayed(end - cs) * delta;
+      tab.to_end[tid] = decayed(end - cs) * fabsf(delta);
       tab.from_end[tid] = decayed(cs - start);
       if (tid == 0) tab.D = D;
     }
@@ -917,7 +930,7 @@ __device__ __forceinline__ void ssdb_task(const SbArgs& a, const MainPlace& pl, 
     const char* const yi = toks + (i + 1) * M::kX;
     f4* const dx_in = reinterpret_cast<f4*>(lds + M::kDx) + w * 256 + lane;  // of the lane's token, as accumulators lie
     float* const col_in = reinterpret_cast<float*>(lds + M::kCol) + w * 64 + lane;
-    const float delta = tab.delta[me];
+    const float delta = own_delta(tab.delta[me]);
     Frag<IO> mine[2];  // the own row of dy (x)
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) mine[kb] = LX::row(MAKES_C ? yi : xi, 16 * w, 32 * kb, l, gg);
@@ -981,7 +994,7 @@ __device__ __forceinline__ void ssdb_task(const SbArgs& a, const MainPlace& pl, 
           const int s = at + j;
           const float wt = decayed(MAKES_C ? cs_me - tab.cs[s] : tab.cs[s] - cs_me);
           const bool keep = MAKES_C ? s <= me && (!SEQ || s >= begin) : s >= me && (!SEQ || s < next);
-          const float cb = keep ? G[0][q][j] : 0.0f, mw = m[o][j] * wt, with_delta = keep ? mw * (MAKES_C ? tab.delta[s] : delta) : 0.0f;
+          const float cb = keep ? G[0][q][j] : 0.0f, mw = m[o][j] * wt, with_delta = keep ? mw * (MAKES_C ? fabsf(tab.delta[s]) : delta) : 0.0f;
           in += s == me ? 0.0f : with_delta * cb;
           P[0][q][j] += with_delta;
           if (!MAKES_C) {
@@ -1286,7 +1299,7 @@ __device__ __forceinline__ void ssdb_mend(const SbArgs& a, int b, int c, int h) 
           for (int k = 0; k < n; ++k) rb = fmaf(R[k], Io<IO>::load(B + t * a.b_row + k), rb);
           sum = fmaf(decayed(cs[kQ - 1] - cs[t]), rb, sum);
         }
-        if (mine) Io<IO>::store(to, fmaf(a.delta[bch * kQ + t], sum, a.D[h] * Io<IO>::load(dy + t * a.dy_row + h * kP)));
+        if (mine) Io<IO>::store(to, fmaf(own_delta(a.delta[bch * kQ + t]), sum, a.D[h] * Io<IO>::load(dy + t * a.dy_row + h * kP)));
       }
     }
     if (t % rep != h % rep) continue;
@@ -1309,7 +1322,7 @@ __device__ __forceinline__ void ssdb_mend(const SbArgs& a, int b, int c, int h) 
         const float own = Io<IO>::load((of_c ? dy + t * a.dy_row : x + t * a.x_row) + hh * kP);
         for (int o = of_c ? first : t; o < (of_c ? t + 1 : last); ++o) {
           const float m = lanes_sum(own * Io<IO>::load((of_c ? x + o * a.x_row : dy + o * a.dy_row) + hh * kP), 64);
-          const float w = decayed(of_c ? cs[t] - cs[o] : cs[o] - cs[t]) * a.delta[bch * kQ + (of_c ? o : t)] * m;
+          const float w = decayed(of_c ? cs[t] - cs[o] : cs[o] - cs[t]) * (of_c ? fabsf(a.delta[bch * kQ + o]) : own_delta(a.delta[bch * kQ + t])) * m;
           for (int i = 0; i < 2; ++i) {
             const int k = lane + 64 * i;
             if (k < n) sum[i] = fmaf(w, Io<IO>::load((of_c ? B + o * a.b_row : C + o * a.c_row) + k), sum[i]);
@@ -1335,8 +1348,8 @@ __global__ __launch_bounds__(kQ) void ssdb_step_kernel(const SbArgs a) {
   const int m = tile * kTile + kTile - 1 - lane;  // from the tile's last token on
   auto tok = [&](int n, int t) { return t < valid ? a.tok[n * a.tok_step + bch * kQ + t] : 0.0f; };
   auto two = [&](int more, int less) { return static_cast<double>(tok(more, m)) + tok(less, m); };
-  const float delta = a.delta[bch * kQ + tid];
-  const bool gone = static_cast<double>(delta) * a.A[h] <= kGone;  // at this token, whose g is 0 times what it would be
+  const float any_delta = a.delta[bch * kQ + tid], delta = own_delta(any_delta);
+  const bool gone = static_cast<double>(fabsf(any_delta)) * a.A[h] <= kGone;  // at this token, whose g is 0 times what it would be
   const bool gone_m = __shfl(static_cast<int>(gone), 63 - lane), gone_next = __shfl(static_cast<int>(gone), (64 - lane) & 63);
   // inside the tile; no term reaches over a document's begin, or over a step of which nothing is left
   const bool cut_m = lane > 0 && (gone_next || (SEQ && a.next[bc * kQ + m] == m + 1));
@@ -1386,7 +1399,8 @@ __global__ __launch_bounds__(kQ) void ssdb_step_kernel(const SbArgs a) {
   double all[3] = {};  // of dA, ddt_bias and dD: terms of either sign, many of which cancel
   if (tid < valid) {
     const float v = Io<IO>::load(static_cast<const T*>(a.dt) + row * a.dt_row + h) + a.dt_bias[h];
-    const double d = (static_cast<double>(a.A[h]) * g + (static_cast<double>(tok(kDirect, tid)) + of_r0)) * (1.0f / (1.0f + expf(-v)));
+    double d = (static_cast<double>(a.A[h]) * g + (static_cast<double>(tok(kDirect, tid)) + of_r0)) * (1.0f / (1.0f + expf(-v)));
+    if (delta != delta) d = delta;  // all that this token is a term of meets a step that is NaN
     Io<IO>::store(static_cast<T*>(a.ddt) + row * a.nheads + h, static_cast<float>(d));
     all[0] = g * delta;
     all[1] = d;
