@@ -390,7 +390,8 @@ Layout layout(int32_t channels, int32_t io_dtype, bool can_vec) {
 
 int64_t blocks(const Layout& l, int64_t rows, bool bwd) {
   const int64_t per = l.wide ? 1 : kWaves * (64 / l.ln), all = (rows + per - 1) / per;
-  const int64_t most = bwd ? 256 * (l.wide ? std::max(1, 1024 / l.threads) : 4) : int64_t{1} << 22;
+  // (a dispatch dimension counts its work-items in 32 bits)
+  const int64_t most = bwd ? 256 * (l.wide ? std::max(1, 1024 / l.threads) : 4) : std::min(int64_t{1} << 22, (int64_t{1} << 31) / l.threads);
   const int64_t turns = (all + most - 1) / most;
   return (all + turns - 1) / turns;
 }
