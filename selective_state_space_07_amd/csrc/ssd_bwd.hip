@@ -556,6 +556,7 @@ __device__ __forceinline__ void ssdb_carry(const SbArgs& a, int u, char* lds) {
   u /= a.ngroups;
   const int c = u % a.nchunks, b = u / a.nchunks;
   const int valid = min(kQ, a.seqlen - c * kQ), rep = a.nheads / a.ngroups;
+  if (b >= a.batch) return;   // the grid is rounded up
   if (from >= valid) return;  // the whole workgroup; its tokens' shares are read by none
   const int h0 = grp * rep + hs * a.cper, h1 = min(h0 + a.cper, (grp + 1) * rep);
   const int64_t row0 = static_cast<int64_t>(b) * a.seqlen + static_cast<int64_t>(c) * kQ;
@@ -703,8 +704,8 @@ __device__ __forceinline__ void ssdb_carry(const SbArgs& a, int u, char* lds) {
 template <int IO, int N, bool SEQ>
 __global__ __launch_bounds__(kMain) void ssdb_carry_kernel(const SbArgs a) {
   __shared__ __attribute__((aligned(512))) char lds[CarryLds<IO, N>::kBytes];
-  const int u = blockIdx.x >> 1;
-  if (blockIdx.x & 1)
+  const int id = blockIdx.y * gridDim.x + blockIdx.x, u = id >> 1;
+  if (id & 1)
     ssdb_carry<IO, N, SEQ, false>(a, u, lds);
   else
     ssdb_carry<IO, N, SEQ, true>(a, u, lds);
@@ -1215,7 +1216,7 @@ __global__ __launch_bounds__(kMain) void ssdb_main_kernel(const SbArgs a) {
   MainPlace pl;
   {
     const int units = a.batch * a.nchunks * a.ngroups * a.hsplit;
-    const int id = blockIdx.x, j = id >> 3;
+    const int id = blockIdx.y * gridDim.x + blockIdx.x, j = id >> 3;
     pl.i = j % kTiles;
     int u = j / kTiles * 8 + (id & 7);
     if (u >= units) return;
@@ -1491,6 +1492,13 @@ Ws layout(int32_t batch, int32_t seqlen, int32_t nheads, int32_t d_state, int32_
   return w;
 }
 
+// n workgroups, and some more that find nothing to do: at most 2^22 along x (a dispatch dimension counts its work-items in
+// 32 bits), the rest along y.
+dim3 grid_of(int64_t n) {
+  const int64_t gx = std::min(n, int64_t{1} << 22);
+  return dim3(static_cast<unsigned>(gx), static_cast<unsigned>((n + gx - 1) / gx));
+}
+
 template <int IO, int N, bool SEQ>
 hipError_t launch_typed(const SsdBwdCall& c, const SbArgs& a) {
   hipError_t e;
@@ -1500,11 +1508,10 @@ hipError_t launch_typed(const SsdBwdCall& c, const SbArgs& a) {
   hipLaunchKernelGGL(ssdb_pass_kernel, dim3(2 * (n4 / kState), a.nheads, a.batch), dim3(kState), 0, c.stream, a, n4);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const int64_t groups = static_cast<int64_t>(a.batch) * a.nchunks * a.ngroups, units = groups * a.hsplit;
-  hipLaunchKernelGGL((ssdb_carry_kernel<IO, N, SEQ>), dim3(static_cast<unsigned>(groups * a.csplit * 2 * (kQ / CarryLds<IO, N>::kRows))), dim3(kMain), 0,
+  hipLaunchKernelGGL((ssdb_carry_kernel<IO, N, SEQ>), grid_of(groups * a.csplit * 2 * (kQ / CarryLds<IO, N>::kRows)), dim3(kMain), 0,
                      c.stream, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  hipLaunchKernelGGL((ssdb_main_kernel<IO, N, SEQ>), dim3(static_cast<unsigned>((units + 7) / 8 * 8 * kTiles)), dim3(kMain), 0,
-                     c.stream, a);
+  hipLaunchKernelGGL((ssdb_main_kernel<IO, N, SEQ>), grid_of((units + 7) / 8 * 8 * kTiles), dim3(kMain), 0, c.stream, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   if (a.hsplit > 1) {
     using T = typename Io<IO>::T;
