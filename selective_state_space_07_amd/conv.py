@@ -50,7 +50,7 @@ def _act(activation):
 def _weights(weight, bias, dev, channels):
     """(taps, the checked weight and bias, their addresses)"""
     weight = _tensor(weight, "weight", _F32, dev)
-    if weight.dim() != 2 or weight.shape[0] != channels:
+    if weight.dim() != 2 or weight.shape[0] != channels or weight.shape[1] < 1:
         raise _b.MambaScanError(2, "weight must be [%d, taps] (got %s)" % (channels, list(weight.shape)))
     weight, wp = _f32(weight, "weight", dev, weight.shape)
     bias, bp = _f32(bias, "bias", dev, (channels,))
