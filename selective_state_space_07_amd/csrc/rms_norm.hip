@@ -436,7 +436,8 @@ size_t rn_part_floats(int64_t rows, int32_t channels, int32_t io_dtype) {
 }
 
 hipError_t launch_rmsnorm(const RnCall& c) {
-  // 16 bytes of each tensor's own type: a piece of eight bfloat16 channels meets a float32 residual as two of four
+  // 16 bytes of each tensor's own type: a piece of eight bfloat16 channels meets a float32 residual as two of four (16384 x
+  // 768, residual rows 772 apart: forward 28 us, gradients 38; by single elements, as where they start off 16 bytes, 36 and 58)
   const int64_t es = c.io_dtype == 0 ? 4 : 2, rs = c.residual_dtype == 0 ? 4 : 2;
   auto fits = [](const void* p, int64_t row_bytes) { return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && row_bytes % 16 == 0); };
   const bool can_vec = fits(c.x, c.x_row * es) && fits(c.residual, c.residual_row * rs) && fits(c.h, c.h_row * rs) &&

@@ -35,9 +35,14 @@
 // a row and a column of m inside a tile, whose difference counts, are summed in
 // float64 (in float32 dA was off by 10^-6 of itself, and by 3 10^-7 so).
 //
-// Measured at 8 x 2048 tokens, 24 heads in one group, d_state 128, bfloat16, 360
-// us: state 60 us (200 MB, 3.3 TB/s), pass 30, carry 78, main 175, step 16, sums
-// 5. The main kernel holds 2 x 64 sums and products in registers and 142 KB of
+// Steps delta A that leave nothing (large or infinite) or that are NaN: the
+// running sums stay numbers, as the state kernel clamps both; what a NaN makes
+// of the tokens that meet its decay is in their delta, and g's running sums start
+// again at a step that leaves nothing, as at a document. That is 0.6% of the time.
+//
+// Measured at 8 x 2048 tokens, 24 heads in one group, d_state 128, bfloat16, 356
+// us (338 to 370 by card): state 60 us (200 MB, 3.3 TB/s), pass 30, carry 78, main
+// 175, step 16, sums 5. The main kernel holds 2 x 64 sums and products in registers and 142 KB of
 // LDS, so two waves on a SIMD, and neither the matrix cores nor memory but what
 // two waves leave of latency bounds it: 12.5 thousand clocks a head, beside 50
 // thousand before and behind the heads. What was gained there: the waves that
@@ -1437,7 +1442,8 @@ __global__ __launch_bounds__(256) void ssdb_join_kernel(int64_t n4, int32_t spli
 }
 
 // Workgroups that share the heads of a group: as many as end first. One takes a CU for itself, and a time of `fixed` heads
-// before and behind its own. (A chunk has kTiles of the main kernel, and two of the carry kernel. Twelve heads in three
+// before and behind its own. (A chunk has kTiles of the main kernel, and two of the carry kernel; in float32 it has four,
+// which are planned as two. Twelve heads in three
 // groups, 2 x 1501 tokens, float32: split in two, which is 288 workgroups, the main kernel took 124 us and a kernel to join them 5, whole 95.)
 int heads_split(int32_t batch, int32_t nchunks, int32_t nheads, int32_t ngroups, int of_chunk, int fixed) {
   const int rep = nheads / ngroups;
