@@ -306,7 +306,8 @@ struct SbArgs {
 };
 // What the step kernel has of each token: its row of m inside its tile (before the token; in two floats, as its column) and over the three tiles before
 // it, nearest first; its column inside its tile and over the tiles behind it; its shares in g of S and, without delta, of
-// R, whether or not these reach it; x . dx without delta and D, but for R's share; dy . x.
+// R, whether or not these reach it; x . dx without delta and D, but for R's share; dy . x. In float32 but for what is inside a
+// tile: the others are sums that count as they are, not their differences, and off by their own float32 sums already.
 enum { kRowIn, kRow1, kRow2, kRow3, kColIn, kColOut, kOfS, kOfR, kDirect, kSkip, kRowInLess, kColInLess, kTokSums };
 
 // Steps of the exponent. Nothing is left of float32 behind one of kGone or less (2^-150 and less); one below kLeast, -infinity
@@ -1418,7 +1419,7 @@ __global__ __launch_bounds__(kQ) void ssdb_step_kernel(const SbArgs a) {
     if (lane == 0) sums[i][tile] = all[i];
   }
   __syncthreads();
-  if (tid < 3) {
+  if (tid < 3) {  // rounded once a chunk, as the outputs are; the chunks' sums are added in float32
     float* to = tid == 0 ? a.pA : tid == 1 ? a.pb : a.pD;
     to[bch] = static_cast<float>((sums[tid][0] + sums[tid][1]) + (sums[tid][2] + sums[tid][3]));
   }
